@@ -248,6 +248,163 @@ int hs2_sparse_attn(const hs2_heads *q_l, const hs2_cache *k_cache, const hs2_ca
                     const int32_t *idx, int32_t idx_stride, hs2_heads *out, void *stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Drafted tokens and a bounded cache.  The pages describe one decoded token per
+ * step over a cache that only grows; the calls below serve steps that verify
+ * several drafted tokens at once (hs2_rope_append, hs2_tree_attn,
+ * hs2_tree_accept) and caches that must not outgrow a budget
+ * (hs2_full_attn_accumulate, hs2_cache_evict).  They read and write the same
+ * paged caches under the same conventions; a page belongs to one sequence.
+ * Where rows move, a key keeps the rotation of the position it was written
+ * for, so positions are given apart from lengths.
+ * ---------------------------------------------------------------------------
+ */
+
+/* Vectors of several tokens per sequence: element (b, i, h, e) is at
+ * (b * tokens + i) * token_stride + h * head_dim + e. */
+typedef struct {
+  void *data;            /* device; 16-byte aligned */
+  int32_t dtype;         /* HS2_F32 (with an HS2_F32 cache) or HS2_BF16 */
+  int32_t batch;
+  int32_t tokens;        /* N: rows of the longest sequence */
+  int32_t num_heads;
+  int32_t head_dim;
+  int64_t token_stride;  /* elements, >= num_heads * head_dim and a multiple of 16 bytes, so a part
+                            of a fused projection's output can be given as it is */
+} hs2_tokens;
+
+/* Scaling of the rotary frequencies f_i = base^(-2i / rot_dim), i < rot_dim / 2. */
+#define HS2_ROPE_PLAIN 0
+#define HS2_ROPE_LINEAR 1 /* f_i / factor */
+#define HS2_ROPE_NTK 2    /* base * factor^(rot_dim / (rot_dim - 2)) in place of base */
+#define HS2_ROPE_YARN 3   /* f_i for pairs that turn more than beta_fast times in original_context,
+                             f_i / factor below beta_slow turns, a linear ramp over i between;
+                             rotated values times 0.1 ln(factor) + 1 */
+#define HS2_ROPE_BANDS 4  /* f_i above high_freq_factor turns in original_context, f_i / factor
+                             below low_freq_factor, linear in the turns between */
+typedef struct {
+  int32_t rot_dim;       /* a multiple of 16, at most 128: the rotated first elements of a head */
+  int32_t scaling;       /* HS2_ROPE_* */
+  double base;           /* > 1 */
+  double factor;         /* >= 1 (all but HS2_ROPE_PLAIN) */
+  double original_context;                  /* > 0 (YARN, BANDS) */
+  double beta_fast, beta_slow;              /* beta_fast > beta_slow > 0 (YARN) */
+  double low_freq_factor, high_freq_factor; /* 0 < low < high (BANDS) */
+} hs2_rope;
+
+/*
+ * Fills `table` (HOST memory, rot_dim / 2 words) with the turns per position of
+ * each pair in units of 2^-64, for hs2_rope_append(), and *rot_scale with the
+ * factor on the rotated values.  Copy the table to the device once.
+ */
+int hs2_rope_table(const hs2_rope *rope, uint64_t *table, float *rot_scale);
+
+/*
+ * Rotary positions on new tokens, and the append of their K/V rows.  For the
+ * n_b new tokens of sequence b (the last n_b of its T_b rows) at positions
+ * p = positions[b, i], every pair (x, y) of the first rot_dim elements of the
+ * query and key heads becomes
+ *     rot_scale * (x cos a - y sin a, y cos a + x sin a),  a = p * turns * 2 pi,
+ * the angle reduced exactly at any position.  Pairs are (e, e + rot_dim / 2), or
+ * (2e, 2e + 1) with `interleaved`.  Queries go to q_out; keys and the values (not
+ * rotated) are written at positions T_b - n_b + i of the caches as
+ * hs2_kv_bridge_append() writes them: fp32, bf16, or E4M3 with scale = max / 448.
+ *
+ *   q          [B, N, Hq, d] or NULL (then q_out is NULL: keys and values only).
+ *   k, v       [B, N, Hkv, d].
+ *   positions  device int32 [B, N]; drafts of a tree share their depth's.
+ *   table, rot_dim, rot_scale  from hs2_rope_table() (the table on the device).
+ *   seq_lens   device int32 [B]: T_b, the new tokens among them, clamped to [0, t_cap].
+ *   num_new    device int32 [B]: n_b, clamped to [0, min(N, T_b)]; NULL: N for all.
+ *   q_out      device [B, N, Hq, d], contiguous, dtype of q; may be q->data when q is
+ *              contiguous.  Rows of tokens i >= n_b are not touched.
+ * A page outside the cache writes no row.  Asynchronous; needs no workspace.
+ */
+int hs2_rope_append(const hs2_tokens *q, const hs2_tokens *k, const hs2_tokens *v, const int32_t *positions,
+                    const uint64_t *table, int32_t rot_dim, int32_t interleaved, float rot_scale,
+                    const int32_t *seq_lens, const int32_t *num_new, const int32_t *page_table, int32_t max_pages,
+                    const hs2_cache *k_cache, const hs2_cache *v_cache, void *q_out, void *stream);
+
+/* Workspace bytes of hs2_tree_attn() for this shape on the current device (0 if invalid). */
+size_t hs2_tree_attn_workspace(int32_t batch, int32_t tokens, int32_t num_kv_heads, int32_t group, int32_t head_dim,
+                               int32_t kv_dtype);
+
+/*
+ * Attention of drafted tokens over the shared cache, for verifying a tree of
+ * drafts in one pass.  Token i < n_b of sequence b attends to the T_b - n_b rows
+ * of the context and to drafts j < n_b with bit j of tree_mask[b, i] set
+ * (normally its ancestors and itself):
+ *     out[b, i, h] = softmax(q k^T / sqrt(d)) v   over what it sees,
+ * zeros when it sees nothing.  The drafts' K/V rows are already in the cache, in
+ * draft order, at positions T_b - n_b .. T_b - 1.  Rows that a token does not see
+ * do not reach its output, whatever they hold.
+ *
+ *   q, out     [B, N, Hq, d], apart from each other, N in [1, 64]; Hq / Hkv in {1, 2, 4, 8, 16, 32} (fp32: at most 8).
+ *              Rows of tokens i >= n_b are not touched.
+ *   num_draft  device int32 [B]: n_b, clamped to [0, min(N, T_b)]; NULL: N for all.
+ *   tree_mask  device uint64 [B, N]; NULL: a chain (each token sees the earlier ones and itself).
+ *   seq_lens, page_table, max_pages, workspace and limits as for hs2_full_attn_select()
+ *   (the size from hs2_tree_attn_workspace(); hs2_workspace_status() reads its flag).
+ */
+int hs2_tree_attn(const hs2_tokens *q, const hs2_cache *k_cache, const hs2_cache *v_cache, const int32_t *seq_lens,
+                  const int32_t *num_draft, const uint64_t *tree_mask, const int32_t *page_table, int32_t max_pages,
+                  hs2_tokens *out, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * After a verification: row T_b - n_b + path[b, i] of the caches moves to
+ * T_b - n_b + i for i < path_len[b], and lens_out[b] = T_b - n_b + path_len[b].
+ *
+ *   path       device int32 [batch, max_path], max_path in [1, 64]: indices of the accepted
+ *              drafts, in the order in which they continue the context (any order: every row
+ *              is read before one is written).  An index outside [0, n_b) moves nothing.
+ *   path_len   device int32 [batch], clamped to [0, n_b].
+ *   num_draft  device int32 [batch]: n_b, clamped to [0, min(max_path, T_b)]; NULL: max_path for all.
+ *   lens_out   device int32 [batch], apart from seq_lens, num_draft and path_len.
+ * The rows behind the new length are not defined.  Asynchronous; needs no workspace.
+ */
+int hs2_tree_accept(const hs2_cache *k_cache, const hs2_cache *v_cache, const int32_t *seq_lens,
+                    const int32_t *num_draft, const int32_t *path, const int32_t *path_len, int32_t batch,
+                    int32_t max_path, const int32_t *page_table, int32_t max_pages, int32_t *lens_out, void *stream);
+
+/*
+ * The full layer's attention without a selection, its weights added to running
+ * sums: out as for hs2_full_attn_select(), and for every kv head and position
+ * t < T_b
+ *     acc[b, h, t] = decay * acc[b, h, t] + w_t,   w_t = the sum over the group's query heads of
+ *                                                  the softmax probability at t;
+ * the newest `fresh` positions start with w_t (their old contents are not read),
+ * so the sums need no initialisation while a cache grows by `fresh` tokens a step.
+ * Positions t >= T_b are not touched.
+ *
+ *   acc        device fp32 [B, Hkv] rows of acc_stride >= t_cap elements.
+ *   Other arguments, the workspace (hs2_full_attn_select_workspace()) and limits as for
+ *   hs2_full_attn_select().
+ */
+int hs2_full_attn_accumulate(const hs2_heads *q, const hs2_cache *k_cache, const hs2_cache *v_cache,
+                             const int32_t *seq_lens, const int32_t *page_table, int32_t max_pages, float decay,
+                             int32_t fresh, float *acc, int64_t acc_stride, hs2_heads *out, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
+/*
+ * Eviction: where T_b > budget, every kv head keeps its newest `window` positions
+ * and, of the others, the budget - window with the largest sums (ties to the
+ * lower position, NaN below everything).  The kept rows (and E4M3 scales, and
+ * sums) move, in position order, to positions 0 .. budget - 1 of the same head,
+ * in place; lens_out[b] = min(T_b, budget).  Heads of one sequence may keep
+ * different positions.  Shorter sequences are not touched.
+ *
+ *   acc        as for hs2_full_attn_accumulate(); only positions below T_b are read.
+ *   budget     >= 1; window in [0, budget].
+ *   kept       device int32 [batch, Hkv, budget]: the kept positions, ascending, -1 behind the
+ *              last (the call's own kernels read it back).
+ *   lens_out   device int32 [batch], apart from seq_lens.
+ * The rows and sums behind the new length are not defined.  Asynchronous; needs no workspace.
+ */
+int hs2_cache_evict(const hs2_cache *k_cache, const hs2_cache *v_cache, const int32_t *seq_lens, int32_t batch,
+                    const int32_t *page_table, int32_t max_pages, float *acc, int64_t acc_stride, int32_t budget,
+                    int32_t window, int32_t *kept, int32_t *lens_out, void *stream);
+
+/*
  * Synchronises `stream`, then reads and clears the workspace's sticky
  * device-error flag: HS2_OK, or HS2_ERR_TIMEOUT if a bounded device wait of
  * an earlier call on this workspace expired.

@@ -10,13 +10,12 @@
 
 #include "hs2.h"
 #include "hs2_fused_tail.cuh"
+#include "hs2_host.h"
 #include "hs2_internal.h"
 
-using namespace hs2;
+namespace hs2 {
 
-namespace {
-
-thread_local char g_err[512] = "";
+static thread_local char g_err[512] = "";
 
 int fail(int code, const char *fmt, ...) {
   va_list ap;
@@ -30,8 +29,11 @@ int cuda_fail(cudaError_t e, const char *what) {
   return fail(HS2_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
+namespace {
 constexpr int kMaxDevices = 64;
 constexpr int kMaxCtasPerSm = 4;  // bound used to size the per-unit record slots
+
+}  // namespace
 
 int sm_count() {
   static int cache[kMaxDevices] = {0};
@@ -44,6 +46,8 @@ int sm_count() {
   }
   return cache[dev];
 }
+
+namespace {
 
 // ---------------------------------------------------------------- TMA encode
 typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
@@ -99,6 +103,8 @@ std::mutex g_map_mu;
 MapEntry g_maps[16];
 int g_map_next = 0;
 
+}  // namespace
+
 int cache_map(CUtensorMap *map, const hs2_cache *c, int box_rows) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) dev = -1;
@@ -118,6 +124,8 @@ int cache_map(CUtensorMap *map, const hs2_cache *c, int box_rows) {
   g_map_next = (g_map_next + 1) % 16;
   return HS2_OK;
 }
+
+namespace {
 
 // ---------------------------------------------------------------- workspace
 struct Layout {
@@ -181,9 +189,11 @@ FullWs bind(const Layout &L, void *ws, int B, int Hkv) {
   return f;
 }
 
+}  // namespace
+
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-int group_ok(int G) { return G == 1 || G == 2 || G == 4 || G == 8 || G == 16 || G == 32; }
+bool group_ok(int G) { return G == 1 || G == 2 || G == 4 || G == 8 || G == 16 || G == 32; }
 
 // Checks a q/out descriptor against the cache; `what` names it in errors.
 int check_heads(const hs2_heads *h, const hs2_cache *k, const char *what) {
@@ -227,6 +237,30 @@ int check_caches(const hs2_cache *k, const hs2_cache *v) {
   }
   return HS2_OK;
 }
+
+int check_pages(const hs2_cache *k, const int32_t *page_table, int32_t max_pages, int32_t batch, int64_t *t_cap) {
+  if (batch < 1) return fail(HS2_ERR_INVALID_ARG, "batch %d", batch);
+  if (batch > kMaxBatchSmem) return fail(HS2_ERR_UNSUPPORTED, "batch %d > %d", batch, kMaxBatchSmem);
+  if (page_table) {
+    if (max_pages < 1) return fail(HS2_ERR_INVALID_ARG, "max_pages %d with a page table", max_pages);
+    *t_cap = (int64_t)max_pages * k->page_size;
+  } else {
+    if (max_pages != 1) return fail(HS2_ERR_INVALID_ARG, "contiguous layout (no page table) needs max_pages == 1");
+    *t_cap = k->page_size;
+    if ((int64_t)batch * k->page_size > k->num_slots)
+      return fail(HS2_ERR_INVALID_ARG, "contiguous layout needs num_slots >= batch * page_size");
+  }
+  if (*t_cap > kMaxContext || (int64_t)batch * ((*t_cap + 15) / 16) * k->num_kv_heads >= (int64_t(1) << 31))
+    return fail(HS2_ERR_UNSUPPORTED, "context capacity %lld too large (max %lld per sequence)", (long long)*t_cap,
+                (long long)kMaxContext);
+  return HS2_OK;
+}
+
+}  // namespace hs2
+
+using namespace hs2;
+
+namespace {
 
 // Consumer warps, pipeline stages and slices per warp of the attention
 // kernel, most preferred first: enough independent work per SM sub-partition
@@ -291,7 +325,8 @@ FullMmaConfig pick_full_config(int D, bool fp8, int page_size, bool paged, int G
 int full_attn_select_impl(const hs2_heads *q, const hs2_cache *k_cache, const hs2_cache *v_cache,
                           const int32_t *seq_lens, const int32_t *page_table, int32_t max_pages, int32_t window,
                           int32_t k_global, int32_t block, hs2_heads *out, int32_t *idx_out, void *workspace,
-                          size_t workspace_bytes, void *stream, void *mark_event, bool fused = false);
+                          size_t workspace_bytes, void *stream, void *mark_event, bool fused = false,
+                          AccumulateParams *accumulate = nullptr);
 
 }  // namespace
 
@@ -343,24 +378,43 @@ int hs2_full_attn_select_blocks(const hs2_heads *q, const hs2_cache *k_cache, co
                                idx_out, workspace, workspace_bytes, stream, nullptr);
 }
 
+int hs2_full_attn_accumulate(const hs2_heads *q, const hs2_cache *k_cache, const hs2_cache *v_cache,
+                             const int32_t *seq_lens, const int32_t *page_table, int32_t max_pages, float decay,
+                             int32_t fresh, float *acc, int64_t acc_stride, hs2_heads *out, void *workspace,
+                             size_t workspace_bytes, void *stream) {
+  AccumulateParams ap{};
+  ap.acc = acc;
+  ap.acc_stride = acc_stride;
+  ap.decay = decay;
+  ap.fresh = fresh;
+  return full_attn_select_impl(q, k_cache, v_cache, seq_lens, page_table, max_pages, 0, 0, 0, out, nullptr, workspace,
+                               workspace_bytes, stream, nullptr, false, &ap);
+}
+
 }  // extern "C"
 
 namespace {
 
-// The full layer, then token-level selection (block = 0) or block-level
-// selection with blocks of `block` positions.
+// The full layer, then token-level selection (block = 0), block-level selection
+// with blocks of `block` positions, or (accumulate) the weights' running sums in
+// place of a selection.
 int full_attn_select_impl(const hs2_heads *q, const hs2_cache *k_cache, const hs2_cache *v_cache,
                           const int32_t *seq_lens, const int32_t *page_table, int32_t max_pages, int32_t window,
                           int32_t k_global, int32_t block, hs2_heads *out, int32_t *idx_out, void *workspace,
-                          size_t workspace_bytes, void *stream, void *mark_event, bool fused) {
+                          size_t workspace_bytes, void *stream, void *mark_event, bool fused,
+                          AccumulateParams *accumulate) {
   int rc;
   if ((rc = check_caches(k_cache, v_cache))) return rc;
   if ((rc = check_heads(q, k_cache, "q"))) return rc;
   if ((rc = check_heads(out, k_cache, "out"))) return rc;
   if (out->batch != q->batch || out->num_heads != q->num_heads || out->dtype != q->dtype)
     return fail(HS2_ERR_INVALID_ARG, "out shape/dtype differs from q");
-  if (!seq_lens || !idx_out) return fail(HS2_ERR_INVALID_ARG, "seq_lens / idx_out is NULL");
-  if (window < 0 || k_global < 0 || (int64_t)window + k_global < 1 || (int64_t)window + k_global > kMaxSelect)
+  if (!seq_lens || (!idx_out && !accumulate)) return fail(HS2_ERR_INVALID_ARG, "seq_lens / idx_out is NULL");
+  if (accumulate) {
+    if (!accumulate->acc || (reinterpret_cast<uintptr_t>(accumulate->acc) & 3))
+      return fail(HS2_ERR_INVALID_ARG, "acc is NULL or misaligned");
+    if (accumulate->fresh < 0) return fail(HS2_ERR_INVALID_ARG, "fresh %d", accumulate->fresh);
+  } else if (window < 0 || k_global < 0 || (int64_t)window + k_global < 1 || (int64_t)window + k_global > kMaxSelect)
     return fail(HS2_ERR_INVALID_ARG, "window %d / k_global %d (need 1 <= window + k_global <= %d)", window,
                 k_global, kMaxSelect);
   const int B = q->batch, Hkv = k_cache->num_kv_heads, G = q->num_heads / Hkv, D = k_cache->head_dim;
@@ -380,6 +434,9 @@ int full_attn_select_impl(const hs2_heads *q, const hs2_cache *k_cache, const hs
     return fail(HS2_ERR_UNSUPPORTED, "context capacity %lld too large (max %lld per sequence)", (long long)t_cap,
                 (long long)kMaxContext);
   if (B > kMaxBatchSmem) return fail(HS2_ERR_UNSUPPORTED, "batch %d > %d", B, kMaxBatchSmem);
+  if (accumulate && accumulate->acc_stride < t_cap)
+    return fail(HS2_ERR_INVALID_ARG, "acc_stride %lld < capacity %lld", (long long)accumulate->acc_stride,
+                (long long)t_cap);
   const bool mma = k_cache->dtype != HS2_F32;
   if (mma && paged && !(ps % 16 == 0 && (ps % 64 == 0 || 64 % ps == 0)))
     return fail(HS2_ERR_UNSUPPORTED, "page_size %d (16, 32 or a multiple of 64)", ps);
@@ -483,6 +540,11 @@ int full_attn_select_impl(const hs2_heads *q, const hs2_cache *k_cache, const hs
   if (mark_event) {
     e = cudaEventRecord(static_cast<cudaEvent_t>(mark_event), s);
     if (e != cudaSuccess) return cuda_fail(e, "recording the mark event");
+  }
+  if (accumulate) {
+    accumulate->sp = sp;
+    e = launch_accumulate(*accumulate, s);
+    return e == cudaSuccess ? HS2_OK : cuda_fail(e, "accumulate launch");
   }
   e = block > 0 ? launch_block_select(sp, block, s) : (fuse ? launch_select_after_score(sp, s) : launch_select(sp, s));
   if (e != cudaSuccess) return cuda_fail(e, "selection launch");

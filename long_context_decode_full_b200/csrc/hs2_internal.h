@@ -188,6 +188,97 @@ size_t bridge_workspace_bytes(int B, int d_model, int N);
 // Splits `workspace` into tickets and partial sums and launches the append.
 cudaError_t launch_bridge(const BridgeParams &p, void *workspace, cudaStream_t s);
 
+// Drafted tokens of one sequence at most (the bits of a tree mask).
+constexpr int kMaxDraft = 64;
+
+// Rotary positions on new tokens, appended to the cache.
+struct RopeParams {
+  const void *q, *k, *v;             // [B * N] tokens of [heads, D], rows `stride` elements apart; q may be NULL
+  int64_t q_stride, k_stride, v_stride;
+  void *q_out;                       // [B, N, Hq, D]
+  const int32_t *positions;          // [B, N]
+  const uint64_t *table;             // [rot / 2] turns per position, 2^-64 units
+  float mscale;
+  int32_t rot, interleaved;
+  const int32_t *seq_lens, *num_new, *page_table;
+  void *ck, *cv;                     // cache rows [num_slots, Hkv, D]
+  float *k_scale, *v_scale;          // E4M3 only
+  int32_t kv_dtype;
+  int32_t B, N, Hq, Hkv, D;
+  int32_t page_size, max_pages;
+  int64_t t_cap, num_slots;
+  int32_t tokens_per_cta;            // set by launch_rope
+};
+cudaError_t launch_rope(const RopeParams &p, int sms, cudaStream_t s);
+
+// The accepted path of a draft moves to its front.
+constexpr int kAcceptScaleHeads = 8;  // heads per CTA of the E4M3 scales' move
+struct AcceptParams {
+  void *k, *v;
+  float *k_scale, *v_scale;
+  const int32_t *seq_lens, *num_draft, *path, *path_len, *page_table;
+  int32_t *lens_out;
+  int32_t B, M, Hkv;
+  int32_t row_bytes;                 // one slot of K or V, all heads
+  int32_t page_size, max_pages;
+  int64_t t_cap, num_slots;
+};
+cudaError_t launch_accept(const AcceptParams &p, bool scales, cudaStream_t s);
+
+// A cache over its budget keeps the largest sums and the window.
+struct EvictParams {
+  void *k, *v;
+  float *k_scale, *v_scale;
+  float *acc;                        // [B, Hkv] rows of acc_stride sums
+  int64_t acc_stride;
+  const int32_t *seq_lens, *page_table;
+  int32_t *kept;                     // [B, Hkv, budget]
+  int32_t *lens_out;
+  int32_t B, Hkv, budget, window;
+  int32_t head_bytes;                // one head's row of K or V
+  int32_t cols;                      // bytes of it per CTA (set by launch_evict)
+  int32_t page_size, max_pages;
+  int64_t t_cap, num_slots;
+};
+cudaError_t launch_evict(const EvictParams &p, bool scales, int sms, cudaStream_t s);
+
+// acc = decay acc + group weights, from the logits of the attention kernels.
+struct AccumulateParams {
+  ScoreParams sp;                    // window 0; no selection
+  float *acc;
+  int64_t acc_stride;
+  float decay;
+  int32_t fresh;                     // the newest tokens, whose sums start at this call
+};
+cudaError_t launch_accumulate(const AccumulateParams &p, cudaStream_t s);
+
+// Attention of drafted tokens over the cache, split over the context.
+struct TreeParams {
+  const void *q;                     // [B * N] tokens of [Hq, D], rows q_stride elements apart
+  int64_t q_stride, out_stride;
+  const void *k, *v;
+  const float *k_scale, *v_scale;
+  const int32_t *seq_lens, *num_draft, *page_table;
+  const uint64_t *mask;              // [B, N] or nullptr: a chain
+  void *out;                         // as q
+  int32_t B, N, Hq, Hkv, G, D;
+  int32_t page_size, max_pages;
+  int64_t t_cap, num_slots;
+  float c2;                          // log2(e) / sqrt(D)
+  int32_t tile;                      // positions per tile
+  int32_t rows;                      // query rows per block (N * G rows per unit)
+  int32_t blocks;                    // row blocks of a unit: CTAs that walk the same tiles
+  int32_t groups;                    // balanced shares of the tile space, `blocks` CTAs each
+  uint32_t *err;                     // workspace: sticky error flag,
+  int32_t *prefix;                   // [B + 1] tiles before sequence b,
+  float *records;                    // [groups][2][blocks] of rows * (D + 2)
+};
+int tree_f32_rows();
+int tree_f32_tile();
+int tree_f32_ctas_per_sm(int D);
+cudaError_t launch_tree_f32(const TreeParams &p, int kv_dtype, cudaStream_t s);
+cudaError_t launch_tree_combine(const TreeParams &p, bool f32, cudaStream_t s);
+
 // Sets the thread's hs2_last_error() text and returns `code`.
 int set_last_error(int code, const char *msg);
 

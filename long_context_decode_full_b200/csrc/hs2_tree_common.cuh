@@ -1,0 +1,79 @@
+// hs2_tree_common.cuh -- what the kernels of the drafted-tree attention agree
+// on: the balanced partition of the tiles, a unit's rows and masks, and the
+// records of units that are cut.
+//
+// A unit is a (sequence, kv head); its query rows are the n drafted tokens'
+// heads of the group, row r = token r / G, head r % G, in blocks of p.rows.
+// Tiles of p.tile positions are ordered by (sequence, kv head, tile) and cut
+// into p.groups equal shares; the p.blocks CTAs of a share walk the same tiles
+// with a row block each, side by side, so the later ones find K and V in L2.
+// A unit inside one share is finished there; one that is cut leaves a record
+// (m, l, o) per share, rows in base-2 exponents: slot 0 if the unit begins the
+// share, else slot 1 (a share cuts at most the unit it begins with and the one
+// it ends with).
+#pragma once
+
+#include "hs2_internal.h"
+
+namespace hs2 {
+
+namespace {
+
+struct TreeShare {
+  int64_t total;  // Hkv * sum_b tiles
+  int32_t groups;
+  __device__ __forceinline__ int64_t start(int64_t c) const { return c * total / groups; }
+  __device__ __forceinline__ int64_t owner(int64_t x) const { return ((x + 1) * groups - 1) / total; }
+};
+
+__device__ __forceinline__ int tree_len(const TreeParams &p, int b) {
+  return clamp_len(__ldg(p.seq_lens + b), (int)p.t_cap);
+}
+// drafted tokens of sequence b, the last n of its T rows
+__device__ __forceinline__ int tree_drafts(const TreeParams &p, int b, int T) {
+  return clamp_len(p.num_draft ? __ldg(p.num_draft + b) : p.N, min(p.N, T));
+}
+// the drafts that token i of sequence b sees
+__device__ __forceinline__ uint64_t tree_bits(const TreeParams &p, int b, int i, int n) {
+  const uint64_t m = p.mask ? __ldg(p.mask + (int64_t)b * p.N + i) : (2ull << i) - 1ull;
+  return n >= 64 ? m : m & ((1ull << n) - 1ull);
+}
+// prefix[b] = tiles before sequence b, by one warp
+__device__ __forceinline__ void tree_prefix(const TreeParams &p, int32_t *prefix) {
+  const int lane = threadIdx.x & 31;
+  int carry = 0;
+  for (int base = 0; base < p.B; base += 32) {
+    const int b = base + lane;
+    int x = b < p.B ? (tree_len(p, b) + p.tile - 1) / p.tile : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (b < p.B) prefix[b + 1] = carry + x;
+    carry += __shfl_sync(0xffffffffu, x, 31);
+  }
+  if (lane == 0) prefix[0] = 0;
+}
+// last sequence b with Hkv * prefix[b] <= x
+__device__ __forceinline__ int tree_seq(const int32_t *prefix, int B, int Hkv, int64_t x) {
+  int lo = 0, hi = B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if ((int64_t)Hkv * prefix[mid] <= x) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+__device__ __forceinline__ int64_t tree_slot(const TreeParams &p, int b, int64_t pos) {
+  const int64_t s = p.page_table == nullptr ? (int64_t)b * p.page_size + pos
+                                            : (int64_t)__ldg(p.page_table + (int64_t)b * p.max_pages + pos / p.page_size) *
+                                                      p.page_size + pos % p.page_size;
+  return s >= 0 && s < p.num_slots ? s : -1;
+}
+__device__ __forceinline__ float *tree_record(const TreeParams &p, int64_t group, int slot, int block) {
+  return p.records + (((size_t)group * 2 + slot) * p.blocks + block) * (size_t)p.rows * (p.D + 2);
+}
+
+}  // namespace
+
+}  // namespace hs2

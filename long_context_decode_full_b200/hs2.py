@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional, Sequence
+from typing import NamedTuple, Optional, Sequence
 
 import torch
 
@@ -34,6 +34,19 @@ class Heads(ctypes.Structure):
                 ("num_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
 
 
+class Tokens(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("batch", ctypes.c_int32),
+                ("tokens", ctypes.c_int32), ("num_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("token_stride", ctypes.c_int64)]
+
+
+class Rope(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("scaling", ctypes.c_int32), ("base", ctypes.c_double),
+                ("factor", ctypes.c_double), ("original_context", ctypes.c_double), ("beta_fast", ctypes.c_double),
+                ("beta_slow", ctypes.c_double), ("low_freq_factor", ctypes.c_double),
+                ("high_freq_factor", ctypes.c_double)]
+
+
 class HS2Error(RuntimeError):
     def __init__(self, code: int, msg: str):
         super().__init__(f"hs2 error {code}: {msg}")
@@ -47,6 +60,8 @@ EXPORTS = ["hs2_full_attn_select_workspace", "hs2_full_attn_select", "hs2_full_a
            "hs2_sparse_attn",
            "hs2_workspace_status", "hs2_selftest_bounded_wait", "hs2_selftest_grid_barrier",
            "hs2_kv_bridge_workspace", "hs2_kv_bridge_append",
+           "hs2_rope_table", "hs2_rope_append", "hs2_tree_attn_workspace", "hs2_tree_attn", "hs2_tree_accept",
+           "hs2_full_attn_accumulate", "hs2_cache_evict",
            "hs2_copy_peak", "hs2_last_error", "hs2_version"]
 
 
@@ -89,6 +104,22 @@ def lib():
         L.hs2_kv_bridge_append.argtypes = [P, I32, I32, P, P, P, P, I32, ctypes.POINTER(Cache),
                                            ctypes.POINTER(Cache), P, SZ, P]
         L.hs2_kv_bridge_append.restype = ctypes.c_int
+        T, C, F = ctypes.POINTER(Tokens), ctypes.POINTER(Cache), ctypes.c_float
+        L.hs2_rope_table.argtypes = [ctypes.POINTER(Rope), P, ctypes.POINTER(F)]
+        L.hs2_rope_table.restype = ctypes.c_int
+        L.hs2_rope_append.argtypes = [T, T, T, P, P, I32, I32, F, P, P, P, I32, C, C, P, P]
+        L.hs2_rope_append.restype = ctypes.c_int
+        L.hs2_tree_attn_workspace.argtypes = [I32, I32, I32, I32, I32, I32]
+        L.hs2_tree_attn_workspace.restype = SZ
+        L.hs2_tree_attn.argtypes = [T, C, C, P, P, P, P, I32, T, P, SZ, P]
+        L.hs2_tree_attn.restype = ctypes.c_int
+        L.hs2_tree_accept.argtypes = [C, C, P, P, P, P, I32, I32, P, I32, P, P]
+        L.hs2_tree_accept.restype = ctypes.c_int
+        L.hs2_full_attn_accumulate.argtypes = [ctypes.POINTER(Heads), C, C, P, P, I32, F, I32, P, I64,
+                                               ctypes.POINTER(Heads), P, SZ, P]
+        L.hs2_full_attn_accumulate.restype = ctypes.c_int
+        L.hs2_cache_evict.argtypes = [C, C, P, I32, P, I32, P, I64, I32, I32, P, P, P]
+        L.hs2_cache_evict.restype = ctypes.c_int
         L.hs2_selftest_bounded_wait.argtypes = [P, SZ, P]
         L.hs2_selftest_bounded_wait.restype = ctypes.c_int
         L.hs2_selftest_grid_barrier.argtypes = [P, SZ, P]
@@ -346,6 +377,251 @@ def kv_bridge_append(hidden, w_k, w_v, k, v, seq_lens, page_table=None, page_siz
     _check(lib().hs2_kv_bridge_append(_ptr(hidden), B, dm, _ptr(w_k), _ptr(w_v), _ptr(seq_lens), _ptr(page_table),
                                       max_pages, ctypes.byref(kc), ctypes.byref(vc), _ptr(workspace),
                                       workspace.numel(), _stream(stream)))
+
+
+# ---------------------------------------------------------------- drafted tokens, bounded caches
+# These calls run on the device that holds the cache, whichever is current, on
+# its current stream unless one is given.  A decode step makes several of them,
+# so their checks are written to cost a microsecond or two.
+_ROPE_SCALING = {None: 0, "none": 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
+
+
+class RopeTable(NamedTuple):
+    """Turns per position of each rotated pair (hs2_rope_table), on the device."""
+    turns: torch.Tensor  # int64 [rot_dim / 2], the bits of the C table
+    rot_dim: int
+    interleaved: bool
+    scale: float
+
+
+def rope_table(rot_dim: int, base: float = 10000.0, interleaved: bool = False, scaling: Optional[str] = None,
+               factor: float = 1.0, original_context: float = 0.0, beta_fast: float = 32.0, beta_slow: float = 1.0,
+               low_freq_factor: float = 1.0, high_freq_factor: float = 4.0, device="cuda") -> RopeTable:
+    """The frequencies of rope_append(): ``rot_dim`` first elements of a head turn, in pairs (e, e + rot_dim / 2) or,
+    ``interleaved``, (2e, 2e + 1).  ``scaling``: None, "linear", "ntk", "yarn" or "bands" (see HS2_ROPE_* in hs2.h).
+    Built on the host and copied once."""
+    if scaling not in _ROPE_SCALING:
+        raise HS2Error(ERR_INVALID_ARG, f"scaling {scaling!r}, expected one of {sorted(map(str, _ROPE_SCALING))}")
+    r = Rope(rot_dim, _ROPE_SCALING[scaling], base, factor, original_context, beta_fast, beta_slow, low_freq_factor,
+             high_freq_factor)
+    turns = torch.empty(64, dtype=torch.int64)
+    scale = ctypes.c_float()
+    _check(lib().hs2_rope_table(ctypes.byref(r), _ptr(turns), ctypes.byref(scale)))
+    return RopeTable(turns[:rot_dim // 2].to(device), rot_dim, bool(interleaved), scale.value)
+
+
+def _arg(name, t, dtype, shape):
+    """The pointer of an optional contiguous array, checked."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        _need(name, t, dtype, shape=shape)
+    return t.data_ptr()
+
+
+def _paged(k, v, k_scale, v_scale, page_table, page_size, B):
+    """Checked cache descriptors, the page table's pointer and max_pages."""
+    shape, pages, max_pages = k.shape, None, 1
+    for name, x in (("k", k), ("v", v)):
+        if x.dtype not in _DTYPE:
+            raise HS2Error(ERR_INVALID_ARG, f"{name}: dtype {x.dtype} is no cache type")
+        if x.dim() != 3 or not x.is_contiguous():
+            raise HS2Error(ERR_INVALID_ARG, f"{name}: expected a contiguous [num_slots, Hkv, d] cache")
+    if page_table is not None:
+        if page_size is None:
+            raise HS2Error(ERR_INVALID_ARG, "page_size is required with a page table")
+        max_pages = page_table.shape[1] if page_table.dim() == 2 else 0
+        pages = _arg("page_table", page_table, torch.int32, (B, max_pages))
+    elif page_size is None:
+        page_size = shape[0] // max(B, 1)
+    ks, vs = _arg("k_scale", k_scale, torch.float32, shape[:2]), _arg("v_scale", v_scale, torch.float32, v.shape[:2])
+    return (Cache(k.data_ptr(), ks, _DTYPE[k.dtype], shape[1], shape[2], page_size, shape[0]),
+            Cache(v.data_ptr(), vs, _DTYPE[v.dtype], v.shape[1], v.shape[2], page_size, v.shape[0]), pages, max_pages)
+
+
+def _tokens(name, x, dtype) -> Tokens:
+    """[B, N, H, d], the heads of a token side by side and its tokens evenly spaced (a slice of a fused projection)."""
+    if x.dtype is not dtype:
+        raise HS2Error(ERR_INVALID_ARG, f"{name}: dtype {x.dtype}, expected {dtype}")
+    if x.dim() != 4:
+        raise HS2Error(ERR_INVALID_ARG, f"{name}: {x.dim()} dimensions, expected [B, N, H, d]")
+    B, N, H, d = x.shape
+    sb, sn, sh, sd = x.stride()
+    stride = sn if N > 1 else (sb if B > 1 else H * d)
+    if (d > 1 and sd != 1) or (H > 1 and sh != d) or (B > 1 and N > 1 and sb != N * sn):
+        raise HS2Error(ERR_INVALID_ARG, f"{name}: strides {x.stride()}, expected heads and tokens in order")
+    return Tokens(x.data_ptr(), _DTYPE[dtype], B, N, H, d, stride)
+
+
+def _device(k, **tensors) -> int:
+    """The CUDA device of the cache, on which every tensor has to be."""
+    i = k.get_device()
+    if i < 0:
+        raise HS2Error(ERR_INVALID_ARG, "k: not on a CUDA device")
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != i:
+            raise HS2Error(ERR_INVALID_ARG, f"{name}: on {t.device}, the cache on {k.device}")
+    return i
+
+
+def _run(call, device, stream, *args):
+    """``call(*args, stream)`` on `device`, on its current stream unless one is given."""
+    if device == torch.cuda.current_device():
+        rc = call(*args, torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            rc = call(*args, torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream)
+    if rc != OK:
+        _check(rc)
+
+
+def _q_dtype(k):
+    return torch.float32 if k.dtype == torch.float32 else torch.bfloat16
+
+
+def rope_append(q, k_new, v_new, positions, table: RopeTable, k, v, seq_lens, page_table=None, page_size=None,
+                num_new=None, k_scale=None, v_scale=None, q_out=None, stream=None):
+    """Rotary positions on new tokens and the append of their K/V rows: q [B, N, Hq, d] (or None), k_new and v_new
+    [B, N, Hkv, d] -- contiguous, or parts of a fused projection -- at int32 ``positions`` [B, N]; the rows go to
+    positions seq_lens[b] - num_new[b] + i of the caches k / v.  Returns the rotated queries (q_out; rows of tokens
+    that a sequence does not have are left as they are)."""
+    kt, vt = _tokens("k_new", k_new, _q_dtype(k)), _tokens("v_new", v_new, _q_dtype(k))
+    B, N = kt.batch, kt.tokens
+    qt = None
+    if q is not None:
+        qt = _tokens("q", q, _q_dtype(k))
+        if q_out is None:
+            q_out = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
+        _arg("q_out", q_out, q.dtype, q.shape)
+    pp, lp = _arg("positions", positions, torch.int32, (B, N)), _arg("seq_lens", seq_lens, torch.int32, (B,))
+    np_ = _arg("num_new", num_new, torch.int32, (B,))
+    kc, vc, pages, max_pages = _paged(k, v, k_scale, v_scale, page_table, page_size, B)
+    device = _device(k, v=v, q=q, k_new=k_new, v_new=v_new, positions=positions, table=table.turns, seq_lens=seq_lens,
+                     num_new=num_new, page_table=page_table, k_scale=k_scale, v_scale=v_scale, q_out=q_out)
+    _run(lib().hs2_rope_append, device, stream, qt, kt, vt, pp, table.turns.data_ptr(), table.rot_dim, table.interleaved,
+         table.scale, lp, np_, pages, max_pages, kc, vc, None if q_out is None else q_out.data_ptr())
+    return q_out
+
+
+def tree_mask(parents) -> torch.Tensor:
+    """int64 [B, N] masks for tree_attn() from parents [B, N] (CPU): parents[b, i] < i is the draft that token i
+    continues, -1 for the context; each token sees its ancestors and itself."""
+    rows = []
+    for row in torch.as_tensor(parents).tolist():
+        m = []
+        for i, p in enumerate(row):
+            if not -1 <= p < i:
+                raise HS2Error(ERR_INVALID_ARG, f"parents: draft {i} continues {p}")
+            m.append((m[p] if p >= 0 else 0) | 1 << i)
+        rows.append([x - (1 << 64) if x >> 63 else x for x in m])
+    return torch.tensor(rows, dtype=torch.int64)
+
+
+def tree_workspace_bytes(batch: int, tokens: int, num_kv_heads: int, group: int, head_dim: int, kv_dtype: int) -> int:
+    return int(lib().hs2_tree_attn_workspace(batch, tokens, num_kv_heads, group, head_dim, kv_dtype))
+
+
+def alloc_tree_workspace(q, k) -> torch.Tensor:
+    """A workspace for tree_attn() of queries like q [B, N, Hq, d] over caches like k."""
+    B, N, Hq, d = q.shape
+    with torch.cuda.device(k.device):
+        n = tree_workspace_bytes(B, N, k.shape[1], Hq // k.shape[1], d, _DTYPE[k.dtype])
+    if n == 0:
+        raise HS2Error(ERR_INVALID_ARG, "invalid workspace shape")
+    return torch.zeros(n, dtype=torch.uint8, device=k.device)
+
+
+def tree_attn(q, k, v, seq_lens, page_table=None, page_size=None, tree_mask=None, num_draft=None, k_scale=None,
+              v_scale=None, out=None, workspace=None, stream=None):
+    """Attention of drafted tokens q [B, N, Hq, d] (N <= 64), whose K/V rows are the last num_draft[b] of the
+    seq_lens[b] rows: each sees the context and the drafts j with bit j of its int64 ``tree_mask`` [B, N] (None: a
+    chain).  Rows of tokens that a sequence does not have are left as they are in ``out``."""
+    qt = _tokens("q", q, _q_dtype(k))
+    B, N = qt.batch, qt.tokens
+    if out is None:
+        out = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
+    ot = _tokens("out", out, q.dtype)
+    mp, lp = _arg("tree_mask", tree_mask, torch.int64, (B, N)), _arg("seq_lens", seq_lens, torch.int32, (B,))
+    np_ = _arg("num_draft", num_draft, torch.int32, (B,))
+    kc, vc, pages, max_pages = _paged(k, v, k_scale, v_scale, page_table, page_size, B)
+    device = _device(k, v=v, q=q, out=out, tree_mask=tree_mask, seq_lens=seq_lens, num_draft=num_draft,
+                     page_table=page_table, k_scale=k_scale, v_scale=v_scale, workspace=workspace)
+    if workspace is None:
+        workspace = alloc_tree_workspace(q, k)
+    _need("workspace", workspace, torch.uint8)
+    _run(lib().hs2_tree_attn, device, stream, qt, kc, vc, lp, np_, mp, pages, max_pages, ot, workspace.data_ptr(),
+         workspace.numel())
+    return out
+
+
+def tree_accept(k, v, seq_lens, path, path_len, page_table=None, page_size=None, num_draft=None, k_scale=None,
+                v_scale=None, lens_out=None, stream=None):
+    """After a verification: the rows of the accepted drafts path[b, :path_len[b]] move to the front of the draft.
+    Returns the new lengths."""
+    _need("path", path, torch.int32, dim=2)
+    B, M = path.shape
+    lp, ap = _arg("seq_lens", seq_lens, torch.int32, (B,)), _arg("path_len", path_len, torch.int32, (B,))
+    np_ = _arg("num_draft", num_draft, torch.int32, (B,))
+    kc, vc, pages, max_pages = _paged(k, v, k_scale, v_scale, page_table, page_size, B)
+    if lens_out is None:
+        lens_out = torch.empty_like(seq_lens)
+    op = _arg("lens_out", lens_out, torch.int32, (B,))
+    device = _device(k, v=v, seq_lens=seq_lens, path=path, path_len=path_len, num_draft=num_draft, page_table=page_table,
+                     k_scale=k_scale, v_scale=v_scale, lens_out=lens_out)
+    _run(lib().hs2_tree_accept, device, stream, kc, vc, lp, np_, path.data_ptr(), ap, B, M, pages, max_pages, op)
+    return lens_out
+
+
+def _sums(acc, B, Hkv):
+    """Row length and pointer of running sums [B, Hkv, capacity]."""
+    _need("acc", acc, torch.float32, dim=3)
+    if acc.shape[:2] != (B, Hkv):
+        raise HS2Error(ERR_INVALID_ARG, f"acc: shape {tuple(acc.shape)}, expected ({B}, {Hkv}, capacity)")
+    return acc.shape[2], acc.data_ptr()
+
+
+def full_attn_accumulate(q, k, v, seq_lens, acc, page_table=None, page_size=None, decay=1.0, fresh=1, k_scale=None,
+                         v_scale=None, out=None, workspace=None, stream=None):
+    """The full layer's attention, its weights added to the running sums acc [B, Hkv, >= capacity] (fp32):
+    acc = decay * acc + weights, the newest ``fresh`` positions starting anew.  Returns (out, acc)."""
+    _need("q", q, _q_dtype(k), dim=3)
+    B, Hq, d = q.shape
+    lp = _arg("seq_lens", seq_lens, torch.int32, (B,))
+    kc, vc, pages, max_pages = _paged(k, v, k_scale, v_scale, page_table, page_size, B)
+    cap, sums = _sums(acc, B, k.shape[1])
+    if out is None:
+        out = torch.empty_like(q)
+    _arg("out", out, q.dtype, q.shape)
+    device = _device(k, v=v, q=q, seq_lens=seq_lens, acc=acc, page_table=page_table, k_scale=k_scale, v_scale=v_scale,
+                     out=out, workspace=workspace)
+    if workspace is None:
+        with torch.cuda.device(device):
+            workspace = alloc_workspace(B, k.shape[1], Hq // k.shape[1], d, kc.page_size * max_pages, k.device)
+    _need("workspace", workspace, torch.uint8)
+    _run(lib().hs2_full_attn_accumulate, device, stream, heads_desc(q), kc, vc, lp, pages, max_pages, decay, fresh, sums,
+         cap, heads_desc(out), workspace.data_ptr(), workspace.numel())
+    return out, acc
+
+
+def cache_evict(k, v, seq_lens, acc, budget, window=128, page_table=None, page_size=None, k_scale=None, v_scale=None,
+                kept=None, lens_out=None, stream=None):
+    """Where a sequence is longer than ``budget``, every kv head keeps its newest ``window`` tokens and the
+    budget - window others with the largest sums in acc [B, Hkv, >= capacity]; their rows, scales and sums move to the
+    front, in order and in place.  Returns (lens_out [B], kept [B, Hkv, budget]: the kept positions, -1 padded)."""
+    _need("seq_lens", seq_lens, torch.int32, dim=1)
+    B, lp = seq_lens.shape[0], seq_lens.data_ptr()
+    kc, vc, pages, max_pages = _paged(k, v, k_scale, v_scale, page_table, page_size, B)
+    Hkv = k.shape[1]
+    cap, sums = _sums(acc, B, Hkv)
+    if kept is None:
+        kept = torch.empty(B, Hkv, max(budget, 0), dtype=torch.int32, device=k.device)
+    if lens_out is None:
+        lens_out = torch.empty_like(seq_lens)
+    kp, op = _arg("kept", kept, torch.int32, (B, Hkv, budget)), _arg("lens_out", lens_out, torch.int32, (B,))
+    device = _device(k, v=v, seq_lens=seq_lens, acc=acc, page_table=page_table, k_scale=k_scale, v_scale=v_scale, kept=kept,
+                     lens_out=lens_out)
+    _run(lib().hs2_cache_evict, device, stream, kc, vc, lp, B, pages, max_pages, sums, cap, budget, window, kp, op)
+    return lens_out, kept
 
 
 def selftest_bounded_wait(workspace: torch.Tensor, stream=None):
