@@ -22,7 +22,8 @@ ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
                 "-I", os.path.join(ROOT, "include"), "-I", CSRC]
 SOURCES = ["hs2_api.cu", "hs2_full_attn.cu", "hs2_select.cu", "hs2_blocks.cu", "hs2_sparse.cu", "hs2_static.cu",
-           "hs2_bridge.cu", "hs2_draft_api.cu", "hs2_rope.cu", "hs2_tree.cu", "hs2_accumulate.cu", "hs2_evict.cu"]
+           "hs2_bridge.cu", "hs2_draft_api.cu", "hs2_rope.cu", "hs2_tree.cu", "hs2_tree_tc.cu",
+           "hs2_accumulate.cu", "hs2_evict.cu"]
 HEADERS = ["hs2_common.cuh", "hs2_internal.h", "hs2_warp_attn.cuh", "hs2_select_common.cuh", "hs2_fused_tail.cuh",
            "hs2_tc.cuh", "hs2_host.h", "hs2_tree_common.cuh"]
 

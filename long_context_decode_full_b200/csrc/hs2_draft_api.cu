@@ -34,20 +34,21 @@ int check_tokens(const hs2_tokens *x, const hs2_cache *k, const char *what) {
 }
 
 struct TreePlan {
-  int tile, rows, blocks, groups;
+  int tile, rows, streams, blocks, groups;
   size_t prefix, records, total;
 };
 
-TreePlan tree_plan(int B, int N, int G, int D) {
+TreePlan tree_plan(int B, int N, int G, int D, bool f32) {
   TreePlan t{};
-  t.tile = tree_f32_tile();
-  t.rows = tree_f32_rows();
-  const int ctas = sm_count() * tree_f32_ctas_per_sm(D);
-  t.blocks = (N * G + t.rows - 1) / t.rows;
-  t.groups = ctas / t.blocks < 1 ? 1 : ctas / t.blocks;
+  t.tile = f32 ? tree_f32_tile() : tree_tc_tile();
+  t.rows = f32 ? tree_f32_rows() : tree_tc_rows();
+  t.streams = f32 ? 1 : 2;
+  const int ctas = sm_count() * (f32 ? tree_f32_ctas_per_sm(D) : 1), per_block = t.rows * t.streams;
+  t.blocks = (N * G + per_block - 1) / per_block;
+  t.groups = ctas / t.blocks < 1 ? 1 : (ctas / t.blocks > kMaxTreeGroups ? kMaxTreeGroups : ctas / t.blocks);
   t.prefix = 256;
   t.records = align256(t.prefix + (size_t)(B + 1) * 4);
-  t.total = align256(t.records + (size_t)t.groups * 2 * t.blocks * t.rows * (D + 2) * 4);
+  t.total = align256(t.records + (size_t)t.groups * 2 * t.blocks * per_block * (D + 2) * 4);
   return t;
 }
 
@@ -170,7 +171,7 @@ size_t hs2_tree_attn_workspace(int32_t batch, int32_t tokens, int32_t num_kv_hea
   if (batch < 1 || batch > kMaxBatchSmem || tokens < 1 || tokens > kMaxDraft || num_kv_heads < 1 || !group_ok(group) ||
       (head_dim != 64 && head_dim != 128) || kv_dtype < HS2_F32 || kv_dtype > HS2_E4M3)
     return 0;
-  return tree_plan(batch, tokens, group, head_dim).total;
+  return tree_plan(batch, tokens, group, head_dim, kv_dtype == HS2_F32).total;
 }
 
 int hs2_tree_attn(const hs2_tokens *q, const hs2_cache *k_cache, const hs2_cache *v_cache, const int32_t *seq_lens,
@@ -196,7 +197,8 @@ int hs2_tree_attn(const hs2_tokens *q, const hs2_cache *k_cache, const hs2_cache
   const int ps = k_cache->page_size;
   if (k_cache->dtype != HS2_F32 && page_table && !(ps % 16 == 0 && (ps % 64 == 0 || 64 % ps == 0)))
     return fail(HS2_ERR_UNSUPPORTED, "page_size %d (16, 32 or a multiple of 64)", ps);
-  const TreePlan plan = tree_plan(q->batch, q->tokens, G, D);
+  const bool f32 = k_cache->dtype == HS2_F32;
+  const TreePlan plan = tree_plan(q->batch, q->tokens, G, D, f32);
   if (!workspace) return fail(HS2_ERR_WORKSPACE, "workspace is NULL");
   if (reinterpret_cast<uintptr_t>(workspace) & 255) return fail(HS2_ERR_WORKSPACE, "workspace not 256-byte aligned");
   if (workspace_bytes < plan.total)
@@ -228,15 +230,26 @@ int hs2_tree_attn(const hs2_tokens *q, const hs2_cache *k_cache, const hs2_cache
   p.c2 = (float)(1.4426950408889634074 / sqrt((double)D));
   p.tile = plan.tile;
   p.rows = plan.rows;
+  p.streams = plan.streams;
   p.blocks = plan.blocks;
   p.groups = plan.groups;
   p.err = reinterpret_cast<uint32_t *>(w);
   p.prefix = reinterpret_cast<int32_t *>(w + plan.prefix);
   p.records = reinterpret_cast<float *>(w + plan.records);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_tree_f32(p, k_cache->dtype, s);
+  cudaError_t e;
+  if (f32) {
+    e = launch_tree_f32(p, s);
+  } else {
+    // boxes of consecutive slots: a page's, up to a tile (without pages a sequence's rows are one run)
+    p.box = p.tile;
+    while (page_table && ps % p.box) p.box /= 2;
+    CUtensorMap tmk, tmv;
+    if ((rc = cache_map(&tmk, k_cache, p.box)) || (rc = cache_map(&tmv, v_cache, p.box))) return rc;
+    e = launch_tree_tc(p, tmk, tmv, k_cache->dtype, s);
+  }
   if (e != cudaSuccess) return cuda_fail(e, "tree-attention launch");
-  e = launch_tree_combine(p, k_cache->dtype == HS2_F32, s);
+  e = launch_tree_combine(p, f32, s);
   return e == cudaSuccess ? HS2_OK : cuda_fail(e, "tree-attention combine launch");
 }
 

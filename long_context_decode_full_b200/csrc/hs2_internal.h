@@ -266,17 +266,22 @@ struct TreeParams {
   int64_t t_cap, num_slots;
   float c2;                          // log2(e) / sqrt(D)
   int32_t tile;                      // positions per tile
-  int32_t rows;                      // query rows per block (N * G rows per unit)
-  int32_t blocks;                    // row blocks of a unit: CTAs that walk the same tiles
+  int32_t box;                       // positions per TMA box
+  int32_t rows, streams;             // query rows per record; records of a CTA: rows * streams query rows per block
+  int32_t blocks;                    // row blocks of a unit (N * G rows): CTAs that walk the same tiles
   int32_t groups;                    // balanced shares of the tile space, `blocks` CTAs each
   uint32_t *err;                     // workspace: sticky error flag,
   int32_t *prefix;                   // [B + 1] tiles before sequence b,
-  float *records;                    // [groups][2][blocks] of rows * (D + 2)
+  float *records;                    // [groups][2][blocks][streams] of rows * (D + 2)
 };
 int tree_f32_rows();
 int tree_f32_tile();
 int tree_f32_ctas_per_sm(int D);
-cudaError_t launch_tree_f32(const TreeParams &p, int kv_dtype, cudaStream_t s);
+cudaError_t launch_tree_f32(const TreeParams &p, cudaStream_t s);
+int tree_tc_rows();
+int tree_tc_tile();
+cudaError_t launch_tree_tc(const TreeParams &p, const CUtensorMap &tmk, const CUtensorMap &tmv, int kv_dtype, cudaStream_t s);
+constexpr int kMaxTreeGroups = 512;  // shares: the joining kernel lists a unit's records in shared memory
 cudaError_t launch_tree_combine(const TreeParams &p, bool f32, cudaStream_t s);
 
 // Sets the thread's hs2_last_error() text and returns `code`.

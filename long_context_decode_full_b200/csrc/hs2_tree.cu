@@ -1,5 +1,5 @@
 // hs2_tree.cu -- attention of a tree of drafted tokens over the cache: the
-// CUDA-core kernel, and the kernel that joins the records of cut units.
+// kernel of fp32 caches, and the one that joins the records of cut units.
 //
 // Token i of sequence b (n drafted tokens, the last n of T rows) attends to the
 // T - n rows of the context and to the drafts j with bit j of its mask set:
@@ -31,29 +31,8 @@ struct TreeF32Smem {
   static size_t bytes(int B) { return kPrefix + (size_t)(B + 1) * 4; }
 };
 
-// 4 elements of a cache row as fp32
-template <int DT>
-__device__ __forceinline__ float4 load_kv4(const void *x, int64_t e, float scale) {
-  if constexpr (DT == HS2_F32) {
-    return __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(x) + e));
-  } else if constexpr (DT == HS2_BF16) {
-    const uint2 u = __ldg(reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(x) + e));
-    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
-                       __uint_as_float(u.y & 0xFFFF0000u));
-  } else {
-    const uint32_t w = __ldg(reinterpret_cast<const uint32_t *>(static_cast<const uint8_t *>(x) + e));
-    uint32_t lo, hi;
-    e4m3x4_to_f16x2x2(w, lo, hi);
-    __half2 a, b;
-    memcpy(&a, &lo, 4);
-    memcpy(&b, &hi, 4);
-    const float2 fa = __half22float2(a), fb = __half22float2(b);
-    return make_float4(fa.x * scale, fa.y * scale, fb.x * scale, fb.y * scale);
-  }
-}
-
-template <int DT, int D>
-__global__ void __launch_bounds__(kThreads) tree_cuda_core_kernel(const TreeParams p) {
+template <int D>
+__global__ void __launch_bounds__(kThreads) tree_f32_kernel(const TreeParams p) {
   using S = TreeF32Smem<D>;
   extern __shared__ __align__(16) uint8_t smem[];
   float *sq = reinterpret_cast<float *>(smem + S::kQ), *sk = reinterpret_cast<float *>(smem + S::kK);
@@ -88,7 +67,8 @@ __global__ void __launch_bounds__(kThreads) tree_cuda_core_kernel(const TreePara
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
       if (row < nrows) {
         const int i = (row0 + row) / p.G, h = kvh * p.G + (row0 + row) % p.G;
-        x = load_kv4<DT == HS2_F32 ? HS2_F32 : HS2_BF16>(p.q, ((int64_t)b * p.N + i) * p.q_stride + h * D + d, 1.f);
+        x = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(p.q) + ((int64_t)b * p.N + i) * p.q_stride +
+                                                   (int64_t)h * D + d));
       }
       *reinterpret_cast<float4 *>(sq + row * S::QS + d) = x;
     }
@@ -111,8 +91,8 @@ __global__ void __launch_bounds__(kThreads) tree_cuda_core_kernel(const TreePara
         const int64_t slot = p0 + row < T ? tree_slot(p, b, p0 + row) : -1;
         if (slot >= 0) {
           const int64_t hrow = slot * p.Hkv + kvh;
-          k4 = load_kv4<DT>(p.k, hrow * D + d, DT == HS2_E4M3 ? __ldg(p.k_scale + hrow) : 1.f);
-          v4 = load_kv4<DT>(p.v, hrow * D + d, DT == HS2_E4M3 ? __ldg(p.v_scale + hrow) : 1.f);
+          k4 = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(p.k) + hrow * D + d));
+          v4 = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(p.v) + hrow * D + d));
         }
         *reinterpret_cast<float4 *>(sk + row * S::QS + d) = k4;
         *reinterpret_cast<float4 *>(sv + row * D + d) = v4;
@@ -200,7 +180,7 @@ __global__ void __launch_bounds__(kThreads) tree_cuda_core_kernel(const TreePara
     }
     const bool whole = i0 == 0 && i1 == nb;
     const bool begins_share = g - (i1 - i0) == share.start(group);
-    float *rec = whole ? nullptr : tree_record(p, group, begins_share ? 0 : 1, block);
+    float *rec = whole ? nullptr : tree_record(p, group, begins_share ? 0 : 1, block, 0);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int row = ty * 4 + i;
@@ -212,12 +192,7 @@ __global__ void __launch_bounds__(kThreads) tree_cuda_core_kernel(const TreePara
 #pragma unroll
         for (int k = 0; k < D / 64; ++k) {
           const float4 x = make_float4(o[i][4 * k] * inv, o[i][4 * k + 1] * inv, o[i][4 * k + 2] * inv, o[i][4 * k + 3] * inv);
-          if constexpr (DT == HS2_F32) {
-            *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at + k * 64 + tx * 4) = x;
-          } else {
-            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + at + k * 64 + tx * 4) =
-                make_uint2(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w));
-          }
+          *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at + k * 64 + tx * 4) = x;
         }
       } else {
         if (tx == 0) {
@@ -226,7 +201,7 @@ __global__ void __launch_bounds__(kThreads) tree_cuda_core_kernel(const TreePara
         }
 #pragma unroll
         for (int k = 0; k < D / 64; ++k)
-          *reinterpret_cast<float4 *>(rec + 2 * kRows + (size_t)row * D + k * 64 + tx * 4) =
+          reinterpret_cast<float4 *>(rec + 2 * kRows)[(size_t)(k * 16 + tx) * kRows + row] =
               make_float4(o[i][4 * k], o[i][4 * k + 1], o[i][4 * k + 2], o[i][4 * k + 3]);
       }
     }
@@ -234,58 +209,63 @@ __global__ void __launch_bounds__(kThreads) tree_cuda_core_kernel(const TreePara
 }
 
 // ------------------------------------------------------------------ combine
-// out = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s over the shares s of a
-// cut unit, in share order; one warp per row.
+// out = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s over the records s of a
+// unit that was not finished by one stream, in the order of its tiles' shares.
+// A warp takes 32 rows and 4 columns, a CTA 32 rows and 32 columns; the records'
+// places are listed in shared memory first.
 constexpr int kCombineWarps = 8;
 
 template <int D, bool F32>
 __global__ void __launch_bounds__(32 * kCombineWarps) tree_combine_kernel(const TreeParams p) {
+  __shared__ int64_t sh_at[2 * kMaxTreeGroups];  // records in floats from the first, -1: none
   griddep_wait();
   griddep_launch_dependents();
   const int kvh = blockIdx.y, b = blockIdx.z, lane = threadIdx.x & 31;
-  const int row = blockIdx.x * kCombineWarps + (threadIdx.x >> 5);
+  const int row0 = blockIdx.x / (D / 32) * 32, col4 = blockIdx.x % (D / 32) * kCombineWarps + (threadIdx.x >> 5);
   const int T = tree_len(p, b), n = tree_drafts(p, b, T);
-  if (row >= n * p.G) return;
+  if (row0 >= n * p.G) return;
   const int64_t total = (int64_t)p.Hkv * p.prefix[p.B];
   const int nb = p.prefix[b + 1] - p.prefix[b];
-  if (nb == 0 || total == 0) return;
+  if (nb == 0) return;
   const TreeShare share{total, p.groups};
   const int64_t U0 = (int64_t)p.Hkv * p.prefix[b] + (int64_t)kvh * nb;
   const int64_t c0 = share.owner(U0), c1 = share.owner(U0 + nb - 1);
-  if (c0 == c1) return;  // finished by its CTA
-  const int block = row / p.rows, r = row % p.rows;
-  auto record = [&](int64_t c) { return tree_record(p, c, c == c0 && share.start(c) < U0 ? 1 : 0, block); };
-  auto holds = [&](int64_t c) { return share.start(c + 1) > share.start(c); };
+  // 32 rows lie in one block, and in one stream's rows
+  const int per_block = p.rows * p.streams, block = row0 / per_block, in_block = row0 % per_block;
+  const bool dealt = min(per_block, n * p.G - block * per_block) > p.rows;  // the streams have rows of their own
+  const int streams = dealt ? 1 : p.streams, s0 = dealt ? in_block / p.rows : 0;
+  const int r = (dealt ? in_block % p.rows : in_block) + lane;
+  if (c0 == c1 && min(streams, nb) == 1) return;  // finished by its CTA
+  const int records = (int)(c1 - c0 + 1) * streams;
+  for (int i = threadIdx.x; i < records; i += 32 * kCombineWarps) {
+    const int64_t c = c0 + i / streams, g0 = share.start(c), g1 = share.start(c + 1);
+    const int64_t tiles = min(g1, U0 + nb) - max(g0, U0);  // of the unit in this share
+    sh_at[i] = tiles > i % streams ? (int64_t)tree_record_at(p, c, g0 < U0 ? 1 : 0, block, s0 + i % streams) : -1;
+  }
+  __syncthreads();
   float M = -INFINITY;
-  for (int64_t c = c0 + lane; c <= c1; c += 32)
-    if (holds(c)) M = fmaxf(M, __ldcg(record(c) + r));
-  M = warp_max(M);
+#pragma unroll 8
+  for (int i = 0; i < records; ++i) M = fmaxf(M, sh_at[i] >= 0 ? __ldcg(p.records + sh_at[i] + r) : -INFINITY);
   const float at = M == -INFINITY ? 0.f : M;
-  float L = 0.f, o[D / 32];
-#pragma unroll
-  for (int k = 0; k < D / 32; ++k) o[k] = 0.f;
-#pragma unroll 4
-  for (int64_t c = c0; c <= c1; ++c) {
-    if (!holds(c)) continue;
-    const float *rec = record(c);
+  float L = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+  for (int i = 0; i < records; ++i) {
+    if (sh_at[i] < 0) continue;
+    const float *rec = p.records + sh_at[i];
     const float w = exp2f(__ldcg(rec + r) - at);
-    L += w * __ldcg(rec + p.rows + r);
-    const float *x = rec + 2 * p.rows + (size_t)r * D + lane * (D / 32);
-    if constexpr (D == 128) {
-      const float4 v = __ldcg(reinterpret_cast<const float4 *>(x));
-      o[0] += w * v.x, o[1] += w * v.y, o[2] += w * v.z, o[3] += w * v.w;
-    } else {
-      const float2 v = __ldcg(reinterpret_cast<const float2 *>(x));
-      o[0] += w * v.x, o[1] += w * v.y;
-    }
+    L = fmaf(w, __ldcg(rec + p.rows + r), L);
+    const float4 v = __ldcg(reinterpret_cast<const float4 *>(rec + 2 * p.rows) + (size_t)col4 * p.rows + r);
+    o[0] = fmaf(w, v.x, o[0]), o[1] = fmaf(w, v.y, o[1]), o[2] = fmaf(w, v.z, o[2]), o[3] = fmaf(w, v.w, o[3]);
   }
+  const int row = row0 + lane;
+  if (row >= n * p.G) return;
   const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
-  const int64_t e = ((int64_t)b * p.N + row / p.G) * p.out_stride + (kvh * p.G + row % p.G) * D + lane * (D / 32);
-#pragma unroll
-  for (int k = 0; k < D / 32; k += 2) {
-    if constexpr (F32) *reinterpret_cast<float2 *>(static_cast<float *>(p.out) + e + k) = make_float2(o[k] * inv, o[k + 1] * inv);
-    else *reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p.out) + e + k) = pack_bf16(o[k] * inv, o[k + 1] * inv);
-  }
+  const int64_t e = ((int64_t)b * p.N + row / p.G) * p.out_stride + (int64_t)(kvh * p.G + row % p.G) * D + col4 * 4;
+  if constexpr (F32)
+    *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + e) = make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
+  else
+    *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + e) =
+        make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv));
 }
 
 }  // namespace
@@ -294,22 +274,17 @@ int tree_f32_rows() { return kRows; }
 int tree_f32_tile() { return kKeys; }
 int tree_f32_ctas_per_sm(int D) { return D == 64 ? 3 : 1; }
 
-cudaError_t launch_tree_f32(const TreeParams &p, int kv_dtype, cudaStream_t s) {
+cudaError_t launch_tree_f32(const TreeParams &p, cudaStream_t s) {
   auto run = [&](auto kern, size_t bytes) {
     const cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kern), (int)bytes);
     if (e != cudaSuccess) return e;
     return launch_ex(kern, dim3((unsigned)(p.groups * p.blocks)), dim3(kThreads), bytes, s, 0, p);
   };
-  if (kv_dtype == HS2_E4M3) return run(tree_cuda_core_kernel<HS2_E4M3, 128>, TreeF32Smem<128>::bytes(p.B));
-  if (kv_dtype == HS2_BF16)
-    return p.D == 64 ? run(tree_cuda_core_kernel<HS2_BF16, 64>, TreeF32Smem<64>::bytes(p.B))
-                     : run(tree_cuda_core_kernel<HS2_BF16, 128>, TreeF32Smem<128>::bytes(p.B));
-  return p.D == 64 ? run(tree_cuda_core_kernel<HS2_F32, 64>, TreeF32Smem<64>::bytes(p.B))
-                   : run(tree_cuda_core_kernel<HS2_F32, 128>, TreeF32Smem<128>::bytes(p.B));
+  return p.D == 64 ? run(tree_f32_kernel<64>, TreeF32Smem<64>::bytes(p.B)) : run(tree_f32_kernel<128>, TreeF32Smem<128>::bytes(p.B));
 }
 
 cudaError_t launch_tree_combine(const TreeParams &p, bool f32, cudaStream_t s) {
-  const dim3 grid((unsigned)((p.N * p.G + kCombineWarps - 1) / kCombineWarps), (unsigned)p.Hkv, (unsigned)p.B), block(32 * kCombineWarps);
+  const dim3 grid((unsigned)((p.N * p.G + 31) / 32 * (p.D / 32)), (unsigned)p.Hkv, (unsigned)p.B), block(32 * kCombineWarps);
   if (f32)
     return p.D == 64 ? launch_ex(tree_combine_kernel<64, true>, grid, block, 0, s, 0, p)
                      : launch_ex(tree_combine_kernel<128, true>, grid, block, 0, s, 0, p);

@@ -3,14 +3,19 @@
 // records of units that are cut.
 //
 // A unit is a (sequence, kv head); its query rows are the n drafted tokens'
-// heads of the group, row r = token r / G, head r % G, in blocks of p.rows.
-// Tiles of p.tile positions are ordered by (sequence, kv head, tile) and cut
-// into p.groups equal shares; the p.blocks CTAs of a share walk the same tiles
-// with a row block each, side by side, so the later ones find K and V in L2.
-// A unit inside one share is finished there; one that is cut leaves a record
-// (m, l, o) per share, rows in base-2 exponents: slot 0 if the unit begins the
-// share, else slot 1 (a share cuts at most the unit it begins with and the one
-// it ends with).
+// heads of the group, row r = token r / G, head r % G, in blocks of p.rows x
+// p.streams.  Tiles of p.tile positions are ordered by (sequence, kv head, tile)
+// and cut into p.groups equal shares; the p.blocks CTAs of a share walk the same
+// tiles with a row block each, side by side, so the later ones find K and V in L2.
+//
+// A CTA has p.streams sets of p.rows running sums.  A block of more than p.rows
+// rows deals its rows to the streams, a smaller one its tiles.  A unit inside one
+// share whose sums are in one stream is finished there; else each stream with
+// tiles leaves a record (m, l, o) per share, rows in base-2 exponents: slot 0 if
+// the unit begins the share, else slot 1 (a share cuts at most the unit it begins
+// with and the one it ends with).  A record is m[rows], l[rows] and o as
+// [D / 4][rows] groups of 4 columns, so that neighbouring rows are written and
+// read side by side.
 #pragma once
 
 #include "hs2_internal.h"
@@ -70,8 +75,11 @@ __device__ __forceinline__ int64_t tree_slot(const TreeParams &p, int b, int64_t
                                                       p.page_size + pos % p.page_size;
   return s >= 0 && s < p.num_slots ? s : -1;
 }
-__device__ __forceinline__ float *tree_record(const TreeParams &p, int64_t group, int slot, int block) {
-  return p.records + (((size_t)group * 2 + slot) * p.blocks + block) * (size_t)p.rows * (p.D + 2);
+__device__ __forceinline__ size_t tree_record_at(const TreeParams &p, int64_t group, int slot, int block, int stream) {
+  return ((((size_t)group * 2 + slot) * p.blocks + block) * p.streams + stream) * (size_t)p.rows * (p.D + 2);
+}
+__device__ __forceinline__ float *tree_record(const TreeParams &p, int64_t group, int slot, int block, int stream) {
+  return p.records + tree_record_at(p, group, slot, block, stream);
 }
 
 }  // namespace
