@@ -48,7 +48,7 @@ TreePlan tree_plan(int B, int N, int G, int D, bool f32) {
   t.groups = ctas / t.blocks < 1 ? 1 : (ctas / t.blocks > kMaxTreeGroups ? kMaxTreeGroups : ctas / t.blocks);
   t.prefix = 256;
   t.records = align256(t.prefix + (size_t)(B + 1) * 4);
-  t.total = align256(t.records + (size_t)t.groups * 2 * t.blocks * per_block * (D + 2) * 4);
+  t.total = align256(t.records + (size_t)t.groups * kTreeSlots * t.blocks * per_block * (D + 2) * 4);
   return t;
 }
 
@@ -244,6 +244,8 @@ int hs2_tree_attn(const hs2_tokens *q, const hs2_cache *k_cache, const hs2_cache
     // boxes of consecutive slots: a page's, up to a tile (without pages a sequence's rows are one run)
     p.box = p.tile;
     while (page_table && ps % p.box) p.box /= 2;
+    p.page_step = p.tile / ps;
+    p.page_off = p.tile % ps;
     CUtensorMap tmk, tmv;
     if ((rc = cache_map(&tmk, k_cache, p.box)) || (rc = cache_map(&tmv, v_cache, p.box))) return rc;
     e = launch_tree_tc(p, tmk, tmv, k_cache->dtype, s);

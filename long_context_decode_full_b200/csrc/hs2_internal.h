@@ -252,6 +252,7 @@ struct AccumulateParams {
 };
 cudaError_t launch_accumulate(const AccumulateParams &p, cudaStream_t s);
 
+constexpr int kTreeSlots = 3;
 // Attention of drafted tokens over the cache, split over the context.
 struct TreeParams {
   const void *q;                     // [B * N] tokens of [Hq, D], rows q_stride elements apart
@@ -267,12 +268,13 @@ struct TreeParams {
   float c2;                          // log2(e) / sqrt(D)
   int32_t tile;                      // positions per tile
   int32_t box;                       // positions per TMA box
+  int32_t page_step, page_off;       // whole pages, and the rest, from one tile to the next
   int32_t rows, streams;             // query rows per record; records of a CTA: rows * streams query rows per block
   int32_t blocks;                    // row blocks of a unit (N * G rows): CTAs that walk the same tiles
   int32_t groups;                    // balanced shares of the tile space, `blocks` CTAs each
   uint32_t *err;                     // workspace: sticky error flag,
   int32_t *prefix;                   // [B + 1] tiles before sequence b,
-  float *records;                    // [groups][2][blocks][streams] of rows * (D + 2)
+  float *records;                    // [groups][kTreeSlots][blocks][streams] of rows * (D + 2)
 };
 int tree_f32_rows();
 int tree_f32_tile();

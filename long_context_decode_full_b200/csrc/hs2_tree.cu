@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kThreads) tree_f32_kernel(const TreeParams p) 
 
 // ------------------------------------------------------------------ combine
 // out = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s over the records s of a
-// unit that was not finished by one stream, in the order of its tiles' shares.
+// cut unit, in the order of its shares.
 // A warp takes 32 rows and 4 columns, a CTA 32 rows and 32 columns; the records'
 // places are listed in shared memory first.
 constexpr int kCombineWarps = 8;
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) tree_combine_kernel(const 
   const bool dealt = min(per_block, n * p.G - block * per_block) > p.rows;  // the streams have rows of their own
   const int streams = dealt ? 1 : p.streams, s0 = dealt ? in_block / p.rows : 0;
   const int r = (dealt ? in_block % p.rows : in_block) + lane;
-  if (c0 == c1 && min(streams, nb) == 1) return;  // finished by its CTA
+  if (c0 == c1) return;  // finished by its CTA
   const int records = (int)(c1 - c0 + 1) * streams;
   for (int i = threadIdx.x; i < records; i += 32 * kCombineWarps) {
     const int64_t c = c0 + i / streams, g0 = share.start(c), g1 = share.start(c + 1);
@@ -243,19 +243,37 @@ __global__ void __launch_bounds__(32 * kCombineWarps) tree_combine_kernel(const 
     sh_at[i] = tiles > i % streams ? (int64_t)tree_record_at(p, c, g0 < U0 ? 1 : 0, block, s0 + i % streams) : -1;
   }
   __syncthreads();
-  float M = -INFINITY;
-#pragma unroll 8
-  for (int i = 0; i < records; ++i) M = fmaxf(M, sh_at[i] >= 0 ? __ldcg(p.records + sh_at[i] + r) : -INFINITY);
-  const float at = M == -INFINITY ? 0.f : M;
-  float L = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-  for (int i = 0; i < records; ++i) {
-    if (sh_at[i] < 0) continue;
-    const float *rec = p.records + sh_at[i];
-    const float w = exp2f(__ldcg(rec + r) - at);
-    L = fmaf(w, __ldcg(rec + p.rows + r), L);
-    const float4 v = __ldcg(reinterpret_cast<const float4 *>(rec + 2 * p.rows) + (size_t)col4 * p.rows + r);
-    o[0] = fmaf(w, v.x, o[0]), o[1] = fmaf(w, v.y, o[1]), o[2] = fmaf(w, v.z, o[2]), o[3] = fmaf(w, v.w, o[3]);
+  // a batch of records at a time, so that their loads are in flight together
+  constexpr int kBatch = 8;
+  float M = -INFINITY, L = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int i0 = 0; i0 < records; i0 += kBatch) {
+    float m[kBatch], l[kBatch];
+    float4 v[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int64_t x = i0 + k < records ? sh_at[i0 + k] : -1;
+      m[k] = -INFINITY, l[k] = 0.f, v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (x >= 0) {
+        const float *rec = p.records + x;
+        m[k] = __ldcg(rec + r);
+        l[k] = __ldcg(rec + p.rows + r);
+        v[k] = __ldcg(reinterpret_cast<const float4 *>(rec + 2 * p.rows) + (size_t)col4 * p.rows + r);
+      }
+    }
+    float top = M;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) top = fmaxf(top, m[k]);
+    const float at = top == -INFINITY ? 0.f : top, alpha = exp2f(M - at);  // the first batch: 0 times 0
+    M = top;
+    L *= alpha;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] *= alpha;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const float w = exp2f(m[k] - at);
+      L = fmaf(w, l[k], L);
+      o[0] = fmaf(w, v[k].x, o[0]), o[1] = fmaf(w, v[k].y, o[1]), o[2] = fmaf(w, v[k].z, o[2]), o[3] = fmaf(w, v[k].w, o[3]);
+    }
   }
   const int row = row0 + lane;
   if (row >= n * p.G) return;

@@ -10,12 +10,12 @@
 //
 // A CTA has p.streams sets of p.rows running sums.  A block of more than p.rows
 // rows deals its rows to the streams, a smaller one its tiles.  A unit inside one
-// share whose sums are in one stream is finished there; else each stream with
-// tiles leaves a record (m, l, o) per share, rows in base-2 exponents: slot 0 if
-// the unit begins the share, else slot 1 (a share cuts at most the unit it begins
-// with and the one it ends with).  A record is m[rows], l[rows] and o as
-// [D / 4][rows] groups of 4 columns, so that neighbouring rows are written and
-// read side by side.
+// share is finished by its CTA; of one that is cut, each stream with tiles leaves
+// a record (m, l, o) per share, rows in base-2 exponents: slot 0 if the unit begins
+// the share, else slot 1 (a share cuts at most the unit it begins with and the one
+// it ends with; slot 2 is the CTA's own, to join its streams).  A record is
+// m[rows], l[rows] and o as [D / 4][rows] groups of 4 columns, so that
+// neighbouring rows are written and read side by side.
 #pragma once
 
 #include "hs2_internal.h"
@@ -76,7 +76,7 @@ __device__ __forceinline__ int64_t tree_slot(const TreeParams &p, int b, int64_t
   return s >= 0 && s < p.num_slots ? s : -1;
 }
 __device__ __forceinline__ size_t tree_record_at(const TreeParams &p, int64_t group, int slot, int block, int stream) {
-  return ((((size_t)group * 2 + slot) * p.blocks + block) * p.streams + stream) * (size_t)p.rows * (p.D + 2);
+  return ((((size_t)group * kTreeSlots + slot) * p.blocks + block) * p.streams + stream) * (size_t)p.rows * (p.D + 2);
 }
 __device__ __forceinline__ float *tree_record(const TreeParams &p, int64_t group, int slot, int block, int stream) {
   return p.records + tree_record_at(p, group, slot, block, stream);

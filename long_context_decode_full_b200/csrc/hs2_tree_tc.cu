@@ -2,17 +2,16 @@
 // cache on the tensor cores (tcgen05, accumulators in tensor memory).
 //
 // A CTA walks the tiles of its share (hs2_tree_common.cuh) with two streams, a
-// warpgroup each, a thread per query row.  Stream s holds 128 logits columns
-// S_s and D output columns O_s of tensor memory and repeats, per tile of 128
-// positions,
-//   S_s = Q_s K^T                       (tcgen05.mma, Q and K in shared memory)
-//   P_s = 2^(c2 S_s - m), l += sum P_s  (registers; P_s as bf16 over S_s's columns)
-//   O_s += P_s V                        (tcgen05.mma, P from tensor memory).
+// warpgroup each, a thread per query row.  Stream s holds 128 logits columns S_s
+// and D output columns O_s of tensor memory and repeats, per tile of 128 positions,
+//   S_s = Q_s K^T                     (tcgen05.mma, Q and K in shared memory)
+//   P_s = 2^(c2 S_s - m), l += sum P  (registers; P as bf16 over S's columns)
+//   O_s += P_s V                      (tcgen05.mma, P from tensor memory).
 // While one stream's warpgroup is at its exponentials the tensor cores work for
-// the other.  A block of more than 128 rows gives each stream 128 of them, and
-// both take every tile; with 128 rows or fewer both hold the same rows and take
-// every other tile, so a memory-bound call has two warpgroups at work, too; the
-// joining kernel adds their sums.
+// the other.  A block of more than 128 rows gives each stream 128 of them, and both
+// take every tile; with 128 rows or fewer both hold the same rows and take every
+// other tile, so a memory-bound call has two warpgroups at work, too; their sums
+// are joined at the end.
 //
 // m moves only when a row's maximum passes it by more than 8 (in base-2
 // exponents): weights stay below 2^8, which bf16 and fp32 sums hold as well as
@@ -27,7 +26,7 @@
 // by a warpgroup of its own, and its scale joins the weight before it is rounded.
 //
 // Roles: warps 0-3 and 4-7 the streams, 8-11 the values (conversion, and rows
-// that must not be multiplied, below), 12 the TMA loads, 13 the MMA issue.
+// that must not be multiplied, below), 12 the TMA loads, 13 the MMA issue, 14 E4M3's scales.
 //
 // Rows of V that a query row must not see, whatever they hold: weight 0 times
 // NaN is NaN in a matrix product, so the values warpgroup clears the rows behind
@@ -59,54 +58,55 @@ struct TreeTc {
   static constexpr int kVals = FP8 ? kKeys * D * 2 : 0;                       // a converted V tile
   static constexpr int kPanel = kKeys * 128;                                  // 128 bytes of every row
   static constexpr int kPanels = kTile / kPanel;
-  static constexpr int kStages = FP8 ? 5 : (D == 128 ? 5 : 8);
-  static constexpr size_t oStage = 2 * kQ, oVals = oStage + (size_t)kStages * kTile, oScale = oVals + 2 * kVals,
-                          oBar = oScale + (FP8 ? 2 * 2 * kKeys * 4 : 0);
-  // full[S], empty[S], q_full[2], s_full[2], p_full[2], o_full[2], v_ready[2], v_free[2], scale_full[2], v_landed[2], done
-  static constexpr int kBars = 2 * kStages + 17;
-  static constexpr size_t oBad = oBar + (size_t)((kBars * 8 + 15) / 16 * 16), oInfo = oBad + 16, kBytes = oInfo + 64 + 1024;
+  static constexpr int kStagesK = FP8 ? 3 : (D == 128 ? 5 : 8), kStagesV = FP8 ? 2 : 0;  // bf16: V has no ring of its own
+  static constexpr int kStages = kStagesK + kStagesV;
+  static constexpr int kSlots = 2;  // tiles in the values warpgroup's hands
+  static constexpr size_t oStage = 2 * kQ, oVals = oStage + (size_t)kStages * kTile, oScale = oVals + kSlots * kVals,
+                          oBar = oScale + (FP8 ? kSlots * 2 * kKeys * 4 : 0);
+  // full[S], empty[S], q_full[2], s_full[2], p_full[2], o_full[2], and per slot v_ready, v_free, scale_full, v_landed; done
+  static constexpr int kBars = 2 * kStages + 8 + 4 * kSlots + 1;
+  static constexpr size_t oBad = oBar + (size_t)((kBars * 8 + 15) / 16 * 16), oInfo = oBad + 8 * kSlots, kBytes = oInfo + 64 + 1024;
   static_assert(kBytes <= 232448, "shared memory of a CTA");
 };
 
-struct TreeInfo {       // shared
-  int64_t total, base;  // tiles; tiles before sequence b0
-  int32_t b0;           // the sequence in which the share begins
+struct TreeInfo {  // shared
+  int32_t g0, g1;  // the share's tiles
+  int32_t b0, base;  // the sequence in which it begins, and the tiles before that
   uint32_t tmem;
   int32_t abort;
 };
 
 // One unit's part in a share.
 struct TreeSeg {
-  int b, kvh, i0, i1, T, n, first, nr;
+  int b, kvh, i0, i1, T, first, nr, special0;  // special0: the first tile with a draft, or rows behind the sequence
   bool pair, begins, whole;
 };
 
+// Tiles are numbered in 32 bits: the entry points keep them below 2^31.
 struct TreeWalk {
-  int64_t g, g0, g1, base;
-  int b;
-  __device__ __forceinline__ TreeWalk(const TreeInfo &in, const TreeShare &share, int64_t group)
-      : g(share.start(group)), g0(g), g1(share.start(group + 1)), base(in.base), b(in.b0) {}
+  int g, g0, g1, base, b;
+  __device__ __forceinline__ explicit TreeWalk(const TreeInfo &in) : g(in.g0), g0(in.g0), g1(in.g1), base(in.base), b(in.b0) {}
   // The next segment that has rows for this CTA.
   __device__ __forceinline__ bool next(const TreeParams &p, int block, TreeSeg &s) {
     while (g < g1 && b < p.B) {
       s.T = tree_len(p, b);
-      const int nb = (s.T + kKeys - 1) / kKeys;
-      const int64_t r = g - base;
-      if (r >= (int64_t)p.Hkv * nb) {
-        base += (int64_t)p.Hkv * nb;
+      const int nb = (s.T + kKeys - 1) / kKeys, r = g - base;
+      if ((int64_t)r >= (int64_t)p.Hkv * nb) {
+        base += p.Hkv * nb;
         ++b;
         continue;
       }
       s.b = b;
-      s.kvh = (int)(r / nb);
-      s.i0 = (int)(r % nb);
-      s.i1 = (int)min((int64_t)nb, s.i0 + (g1 - g));
-      s.n = tree_drafts(p, b, s.T);
-      s.first = s.T - s.n;
+      s.kvh = r / nb;
+      s.i0 = r - s.kvh * nb;
+      s.i1 = min(nb, s.i0 + (g1 - g));
+      const int n = tree_drafts(p, b, s.T);
+      s.first = s.T - n;
+      s.special0 = max(s.i0, min(s.i1, s.first / kKeys));
       s.begins = g == g0;
       s.whole = s.i0 == 0 && s.i1 == nb;
       g += s.i1 - s.i0;
-      s.nr = min(2 * kStreamRows, s.n * p.G - block * 2 * kStreamRows);
+      s.nr = min(2 * kStreamRows, n * p.G - block * 2 * kStreamRows);
       s.pair = s.nr > kStreamRows;
       if (s.nr > 0) return true;
     }
@@ -114,30 +114,51 @@ struct TreeWalk {
   }
 };
 
-// The loads of a segment: K of the first `ahead` tiles, then V of tile i and K of
-// tile i + ahead; and the stages that hold them.  bf16: one ring in this order.
-// E4M3: a ring for K (3 stages) and one for V (2), because the values warpgroup
-// waits for V alone, and a waiter that misses a stage's phases cannot tell them apart.
-template <bool FP8, int S>
-struct TreeOrder {
-  int nt, ahead;
-  uint32_t before;  // tiles of the CTA's earlier segments
-  __device__ __forceinline__ TreeOrder(const TreeSeg &s, uint32_t tiles)
-      : nt(s.i1 - s.i0), ahead(min(s.pair ? 1 : 2, nt)), before(tiles) {}
-  struct Place {
-    uint32_t stage, parity;
-  };
-  __device__ __forceinline__ Place v(int i) const {
-    if constexpr (FP8) return {3u + ((before + i) & 1u), ((before + i) >> 1) & 1u};
-    const uint32_t at = 2 * before + ahead + i + min(i, nt - ahead);
-    return {at % S, (at / S) & 1u};
+// The pages of one row of every tile of a sequence, in tile order; the page numbers are fetched apart from their use.
+struct TreePages {
+  const int32_t *row;  // the next tile's page number
+  int off, pos;        // the row's place in its page, and in the sequence
+  __device__ __forceinline__ TreePages(const TreeParams &p, const TreeSeg &s, int first) : pos(s.i0 * kKeys + first) {
+    const int page = pos / p.page_size;
+    off = pos - page * p.page_size;
+    row = p.page_table ? p.page_table + (int64_t)s.b * p.max_pages + page : nullptr;
   }
-  __device__ __forceinline__ Place k(int i) const {
-    if constexpr (FP8) return {(before + i) % 3u, ((before + i) / 3u) & 1u};
-    const uint32_t at = 2 * before + (i < ahead ? i : i + 1 + min(i - ahead, nt - ahead));
-    return {at % S, (at / S) & 1u};
+  struct Row {
+    int page, off;  // off < 0: behind the sequence
+  };
+  __device__ __forceinline__ Row next(const TreeParams &p, int T) {
+    Row r{0, off};
+    if (pos >= T) r.off = -1;
+    else if (row) r.page = __ldg(row);
+    pos += kKeys;
+    off += p.page_off;
+    if (row) row += p.page_step;
+    if (off >= p.page_size) {
+      off -= p.page_size;
+      if (row) ++row;
+    }
+    return r;
+  }
+  // the slot in the cache, or -1
+  static __device__ __forceinline__ int64_t slot(const TreeParams &p, const TreeSeg &s, Row r) {
+    const int64_t x = (int64_t)(p.page_table ? r.page : s.b) * p.page_size + r.off;
+    return r.off >= 0 && x >= 0 && x < p.num_slots ? x : -1;
   }
 };
+
+// The loads of a segment, and the order in which the products use them: K of the
+// first `ahead` tiles, then V of tile i and K of tile i + ahead.  bf16: one ring of
+// stages in this order.  E4M3: a ring for K and one for V, because
+// the values warpgroup waits for V alone, and a waiter that misses a stage's phases
+// cannot tell them apart.
+struct TreeRing {
+  uint32_t stage, parity;
+  template <int FIRST, int STAGES>
+  __device__ __forceinline__ void next() {
+    if (++stage == FIRST + STAGES) stage = FIRST, parity ^= 1u;
+  }
+};
+__device__ __forceinline__ int tree_ahead(const TreeSeg &s) { return min(s.pair ? 1 : 2, s.i1 - s.i0); }
 
 __device__ __forceinline__ void wait_or_abort(uint64_t *bar, uint32_t parity, volatile int32_t *abort, uint32_t *err,
                                               uint32_t bit) {
@@ -169,6 +190,56 @@ __device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;" : "=r"(r) : "r"(taddr) : "memory");
   return r;
 }
+// 4 bytes, or zeros with bytes = 0
+__device__ __forceinline__ void cp_async_4_or_zero(uint32_t dst, const void *src, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+// 64 columns
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
+  uint32_t r[64];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%2"
+      "7,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%5"
+      "2,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]),
+        "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]),
+        "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]),
+        "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]),
+        "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
+}
+// two products, sums or both at once
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
 // 32 columns of packed weights
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
   asm volatile(
@@ -182,19 +253,45 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// D += A B with A (bf16) in tensor memory
-__device__ __forceinline__ void mma_ts_f16(uint32_t d, uint32_t a, uint64_t b, uint32_t id) {
+// Shared-memory descriptors of 128-byte-swizzled operands (hs2_tc.cuh) as two
+// words: the upper one is the same for all (1 KB between groups of 8 rows), the
+// lower one holds the address and, for an MN-major operand, the panels' distance.
+constexpr uint32_t kDescHi = (1024u >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t panel) { return (addr >> 4) | (panel >> 4) << 16; }
+// The whole warp gets here and one lane issues: addresses stay in uniform registers.
+__device__ __forceinline__ void mma_ts_f16(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t one) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d), "r"(a), "l"(b), "r"(id), "r"(1u)
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %4, 0x7fffffff;\n\tsetp.ne.b32 q, %4, 0;\n\tmov.b64 db, {%2, %5};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}\n" ::"r"(d), "r"(a), "r"(b), "r"(id), "r"(one), "r"(kDescHi)
       : "memory");
 }
-__device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+template <bool E4M3>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc, uint32_t one) {
+  if constexpr (E4M3)
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "mov.b64 da, {%1, %6};\n\tmov.b64 db, {%2, %6};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, p;\n\t}\n" ::"r"(d), "r"(a), "r"(b), "r"(id), "r"(acc), "r"(one), "r"(kDescHi)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "mov.b64 da, {%1, %6};\n\tmov.b64 db, {%2, %6};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}\n" ::"r"(d), "r"(a), "r"(b), "r"(id), "r"(acc), "r"(one), "r"(kDescHi)
+        : "memory");
+}
+__device__ __forceinline__ void commit_one(uint32_t bar, uint32_t one) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d), "l"(a), "l"(b), "r"(id), "r"(acc)
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(bar), "r"(one)
       : "memory");
 }
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 // the drafts' bits of 64 columns of a tile, the first draft at column r
 __device__ __forceinline__ uint64_t shift_bits(uint64_t bits, int r) {
@@ -226,8 +323,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::oBar);
+  constexpr int kSlots = C::kSlots, SK = C::kStagesK, SV = C::kStagesV;
   uint64_t *full = bars, *empty = bars + S, *q_full = bars + 2 * S, *s_full = q_full + 2, *p_full = q_full + 4,
-           *o_full = q_full + 6, *v_ready = q_full + 8, *v_free = q_full + 10, *scale_full = q_full + 12, *v_landed = q_full + 14, *done = q_full + 16;
+           *o_full = q_full + 6, *v_ready = q_full + 8, *v_free = v_ready + kSlots, *scale_full = v_free + kSlots,
+           *v_landed = scale_full + kSlots, *done = v_landed + kSlots;
   volatile uint64_t *bad_rows = reinterpret_cast<volatile uint64_t *>(smem + C::oBad);
   TreeInfo *info = reinterpret_cast<TreeInfo *>(smem + C::oInfo);
   volatile int32_t *abort = &info->abort;
@@ -239,11 +338,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < 2; ++s) {
       mbar_init(q_full + s, 4);
       mbar_init(p_full + s, 4);
-      mbar_init(scale_full + s, 128);
     }
+    for (int s = 0; s < kSlots; ++s) mbar_init(scale_full + s, 32);
     fence_mbar_init();
     info->abort = 0;
-    info->total = 0;
+    info->g0 = info->g1 = 0;
   }
   if (warp == 12 && lane == 0) {
     prefetch_tensormap(&tmk);
@@ -272,18 +371,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         sum += carry;
         if (sum - x <= g0 && g0 < sum) {  // one lane of one round, if the share is not empty
-          info->base = sum - x;
+          info->base = (int32_t)(sum - x);
           info->b0 = b0 + lane;
         }
         carry = __shfl_sync(0xffffffffu, sum, 31);
         if (carry > g0) break;
       }
-      if (lane == 0) info->total = share.start(group + 1) > g0 ? total : 0;
+      if (lane == 0) {
+        info->g0 = (int32_t)g0;
+        info->g1 = (int32_t)share.start(group + 1);
+      }
     }
     if (blockIdx.x == 0) tree_prefix(p, p.prefix);
   }
   __syncthreads();
-  if (info->total == 0) return;  // no tiles for this CTA
+  if (info->g0 >= info->g1) return;  // no tiles for this CTA
   if (warp == 13) {
     tc::tmem_alloc(&info->tmem, kTmemCols);
     tc::tmem_relinquish();
@@ -292,8 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = info->tmem;
-  const TreeShare share{info->total, p.groups};
-  TreeWalk walk(*info, share, group);
+  TreeWalk walk(*info);
   TreeSeg seg;
   const int wg = warp >> 2;
 
@@ -304,19 +405,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
     const uint32_t ts = tmem + lanes + (uint32_t)(s * kKeys), to = tmem + lanes + 256u + (uint32_t)(s * D);
     uint8_t *sq = smem + s * C::kQ;
+    bool handed = false;  // a record of sums that stream 0 may still read
     uint32_t ns = 0, handled0 = 0;  // tiles of this stream; tiles handled by the values warpgroup before the segment
     while (walk.next(p, block, seg)) {
       const int nt = seg.i1 - seg.i0;
-      const int special0 = max(seg.i0, min(seg.i1, seg.first / kKeys));  // first tile with a draft (or the tail)
-      const uint32_t handled_here = FP8 ? nt : seg.i1 - special0;
+      const uint32_t handled_here = FP8 ? nt : seg.i1 - seg.special0;
       if (!seg.pair && s >= nt) {  // one tile: the other stream has it
         handled0 += handled_here;
         continue;
       }
       const int r = block * 2 * kStreamRows + (seg.pair ? s * kStreamRows : 0) + row;
-      const bool mine = r < seg.n * p.G, busy = __any_sync(0xffffffffu, mine);
+      const int n = seg.T - seg.first;
+      const bool mine = r < n * p.G, busy = __any_sync(0xffffffffu, mine);
       const int tok = r / p.G, head = seg.kvh * p.G + r % p.G;
-      const uint64_t bits = mine ? tree_bits(p, seg.b, tok, seg.n) : 0ull;
+      const uint64_t bits = mine ? tree_bits(p, seg.b, tok, n) : 0ull;
       float c2 = p.c2;
       // the query row to shared memory, 128-byte swizzle
       if (mine) {
@@ -384,49 +486,51 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool first_tile = true;
       for (int i = seg.pair ? 0 : s; i < nt; i += seg.pair ? 1 : 2) {
         const int t0 = (seg.i0 + i) * kKeys;
-        const bool special = seg.i0 + i >= special0;
-        const uint32_t hc = handled0 + (FP8 ? i : seg.i0 + i - special0);  // this tile among the handled ones
-        wait_or_abort(s_full + s, ns & 1, abort, p.err, kErrFullWait);
+        const bool special = seg.i0 + i >= seg.special0;
+        const uint32_t hc = handled0 + (FP8 ? i : seg.i0 + i - seg.special0);  // this tile among the handled ones
+        const uint32_t slot_id = hc % kSlots, slot_parity = hc / kSlots & 1u;
+        wait_or_abort(s_full + s, ns & 1u, abort, p.err, kErrFullWait);
         tc::fence_after();
-        if (FP8) wait_or_abort(scale_full + (hc & 1), (hc >> 1) & 1, abort, p.err, kErrFullWait);
-        if (special) wait_or_abort(v_ready + (hc & 1), (hc >> 1) & 1, abort, p.err, kErrFullWait);
+        if (FP8) wait_or_abort(scale_full + slot_id, slot_parity, abort, p.err, kErrFullWait);
+        if (special) wait_or_abort(v_ready + slot_id, slot_parity, abort, p.err, kErrFullWait);
         if (busy) {
-          float x[4][32];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tc::ld32(ts + 32 * c, x[c]);
-          const float *ks = reinterpret_cast<const float *>(smem + C::oScale) + (hc & 1) * 2 * kKeys, *vs = ks + kKeys;
+          float x[2][64];
+          tmem_ld64(ts, x[0]);
+          tmem_ld64(ts + 64, x[1]);
+          const float *ks = reinterpret_cast<const float *>(smem + C::oScale) + slot_id * 2 * kKeys, *vs = ks + kKeys;
           if constexpr (FP8) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-              for (int e = 0; e < 32; e += 4) {
-                const float4 f = *reinterpret_cast<const float4 *>(ks + 32 * c + e);
-                x[c][e] *= f.x, x[c][e + 1] *= f.y, x[c][e + 2] *= f.z, x[c][e + 3] *= f.w;
+              for (int e = 0; e < 64; e += 4) {
+                const float4 f = *reinterpret_cast<const float4 *>(ks + 64 * h + e);
+                const float2 u = mul2(make_float2(x[h][e], x[h][e + 1]), make_float2(f.x, f.y));
+                const float2 w = mul2(make_float2(x[h][e + 2], x[h][e + 3]), make_float2(f.z, f.w));
+                x[h][e] = u.x, x[h][e + 1] = u.y, x[h][e + 2] = w.x, x[h][e + 3] = w.y;
               }
           }
           uint64_t seen[2] = {~0ull, ~0ull};
           if (special) {
-            const int rel = seg.first - t0;
-            seen[0] = below(rel) | shift_bits(bits, rel);
-            seen[1] = below(rel - 64) | shift_bits(bits, rel - 64);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const uint32_t w = (uint32_t)(seen[c >> 1] >> (32 * (c & 1)));
+            for (int h = 0; h < 2; ++h) {
+              const int rel = seg.first - t0 - 64 * h;
+              seen[h] = below(rel) | shift_bits(bits, rel);
+              const uint32_t lo = (uint32_t)seen[h], hi = (uint32_t)(seen[h] >> 32);
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (!((w >> e) & 1u)) x[c][e] = -INFINITY;
+              for (int e = 0; e < 64; ++e)
+                if (!(((e < 32 ? lo : hi) >> (e & 31)) & 1u)) x[h][e] = -INFINITY;
             }
           }
-          float mx[4];
+          float mx[8];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            mx[c] = x[c][0];
+          for (int c = 0; c < 8; ++c) {
+            mx[c] = fmaxf(x[0][c], x[1][c]);
 #pragma unroll
-            for (int e = 1; e < 32; ++e) mx[c] = fmaxf(mx[c], x[c][e]);
+            for (int e = 8; e < 64; e += 8) mx[c] = fmaxf(fmaxf(mx[c], x[0][c + e]), x[1][c + e]);
           }
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
           const bool grow = m == -INFINITY ? top > -INFINITY : top > m + growth;
-          const uint64_t bad = special ? bad_rows[hc & 1] : 0ull;
+          const uint64_t bad = special ? bad_rows[slot_id] : 0ull;
           if (__any_sync(0xffffffffu, grow) || bad) {
             float alpha = 1.f;
             if (grow) {
@@ -436,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
             if (!first_tile) {
-              wait_or_abort(o_full + s, (ns - 1) & 1, abort, p.err, kErrFullWait);  // the last product is in O
+              wait_or_abort(o_full + s, (ns - 1) & 1u, abort, p.err, kErrFullWait);  // the last product is in O
               tc::fence_after();
 #pragma unroll 1
               for (int c = 0; c < D; c += 32) {
@@ -449,29 +553,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           const float shift = m == -INFINITY ? 0.f : -m * c2;  // nothing seen yet: weights 0
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
+          const float2 cc = make_float2(c2, c2), sh = make_float2(shift, shift);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint32_t w[32];
 #pragma unroll
             for (int e = 0; e < 64; e += 2) {
-              float a = ex2_approx(fmaf(x[2 * h + (e >> 5)][e & 31], c2, shift));
-              float b = ex2_approx(fmaf(x[2 * h + (e >> 5)][(e & 31) + 1], c2, shift));
-              sum[(e >> 1) & 3] += a + b;
+              float2 a = fma2(make_float2(x[h][e], x[h][e + 1]), cc, sh);
+              a.x = ex2_approx(a.x), a.y = ex2_approx(a.y);
+              sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], a);
               if constexpr (FP8) {
-                const float2 f = *reinterpret_cast<const float2 *>(vs + 64 * h + e);
-                a *= f.x, b *= f.y;
+                a = mul2(a, *reinterpret_cast<const float2 *>(vs + 64 * h + e));
                 if (special) {  // a scale that is not seen may be anything
-                  a = (seen[h] >> e) & 1ull ? a : 0.f;
-                  b = (seen[h] >> (e + 1)) & 1ull ? b : 0.f;
+                  a.x = (seen[h] >> e) & 1ull ? a.x : 0.f;
+                  a.y = (seen[h] >> (e + 1)) & 1ull ? a.y : 0.f;
                 }
               }
-              w[e >> 1] = pack_bf16(a, b);
+              w[e >> 1] = pack_bf16(a.x, a.y);
             }
             tmem_st32(ts + 32 * h, w);
           }
           tmem_wait_st();
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
           if (bad) {  // rare: drafts whose values are not finite, for the rows that see them
             for (uint64_t rest = bad; rest; rest &= rest - 1) {
               const int j = __ffsll((long long)rest) - 1, c = seg.first + j - t0;
@@ -508,18 +612,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(p_full + s);
       }
       handled0 += handled_here;
-      wait_or_abort(o_full + s, (ns - 1) & 1, abort, p.err, kErrFullWait);
+      wait_or_abort(o_full + s, (ns - 1) & 1u, abort, p.err, kErrFullWait);
       tc::fence_after();
-      if (busy) {
-        const bool direct = seg.whole && (seg.pair || nt == 1);
-        float *rec = tree_record(p, group, seg.begins ? 0 : 1, block, s);
-        const float inv = l > 0.f || l != l ? 1.f / l : 0.f;  // nothing seen: zeros
-        if (mine && !direct) {
+      // A unit inside the share is finished here, by stream 0: of a unit whose tiles both streams took, stream 1 hands
+      // its sums over in a record of their own, which stream 0 has read before stream 1 writes the next.
+      const bool join = seg.whole && !seg.pair && nt > 1, finish = seg.whole && !(join && s == 1);
+      if (join && s == 1 && handed) asm volatile("bar.sync 3, 256;" ::: "memory");
+      float *rec = tree_record(p, group, join ? 2 : (seg.begins ? 0 : 1), block, join ? 1 : s);
+      float4 *ro = reinterpret_cast<float4 *>(rec + 2 * kStreamRows) + row;
+      if (busy && !finish) {
+        if (mine) {
           rec[row] = m * c2;
           rec[kStreamRows + row] = l;
         }
-        __syncwarp();
-        float4 *ro = reinterpret_cast<float4 *>(rec + 2 * kStreamRows) + row;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float o[32];
+          __syncwarp();
+          tc::ld32(to + c, o);
+          if (mine) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              ro[(size_t)((c + e) / 4) * kStreamRows] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          }
+        }
+      }
+      if (join && s == 1) asm volatile("bar.arrive 2, 256;" ::: "memory");
+      if (join && s == 0) asm volatile("bar.sync 2, 256;" ::: "memory");
+      if (busy && finish) {
+        float w0 = 1.f, w1 = 0.f, sum = l;
+        if (join && mine) {
+          const float m0 = m * c2, m1 = __ldcg(rec + row), M = fmaxf(m0, m1), at = M == -INFINITY ? 0.f : M;
+          w0 = ex2_approx(m0 - at);
+          w1 = ex2_approx(m1 - at);
+          sum = w0 * l + w1 * __ldcg(rec + kStreamRows + row);
+        }
+        const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;  // nothing seen: zeros
+        w0 *= inv, w1 *= inv;
         uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) +
                                                ((int64_t)seg.b * p.N + tok) * p.out_stride + (int64_t)head * D);
 #pragma unroll 1
@@ -527,216 +656,262 @@ __global__ void __launch_bounds__(kThreads, 1)
           float o[32];
           __syncwarp();
           tc::ld32(to + c, o);
-          if (mine && direct) {
+          if (mine) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] *= w0;
+            if (join) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) {
+                const float4 v = __ldcg(ro + (size_t)((c + e) / 4) * kStreamRows);
+                o[e] = fmaf(w1, v.x, o[e]), o[e + 1] = fmaf(w1, v.y, o[e + 1]);
+                o[e + 2] = fmaf(w1, v.z, o[e + 2]), o[e + 3] = fmaf(w1, v.w, o[e + 3]);
+              }
+            }
 #pragma unroll
             for (int e = 0; e < 32; e += 8)
-              dst[(c + e) / 8] = make_uint4(pack_bf16(o[e] * inv, o[e + 1] * inv), pack_bf16(o[e + 2] * inv, o[e + 3] * inv),
-                                            pack_bf16(o[e + 4] * inv, o[e + 5] * inv), pack_bf16(o[e + 6] * inv, o[e + 7] * inv));
-          } else if (mine) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              ro[(size_t)((c + e) / 4) * kStreamRows] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+              dst[(c + e) / 8] = make_uint4(pack_bf16(o[e], o[e + 1]), pack_bf16(o[e + 2], o[e + 3]),
+                                            pack_bf16(o[e + 4], o[e + 5]), pack_bf16(o[e + 6], o[e + 7]));
           }
         }
       }
+      if (join && s == 0) asm volatile("bar.arrive 3, 256;" ::: "memory");
+      handed = handed || (join && s == 1);
     }
+    if (handed) asm volatile("bar.sync 3, 256;" ::: "memory");
   } else if (wg == 2) {
     // ------------------------------------------------------------ values
     regs_dec<kRegsOther>();
-    const int r = tid & 127;
+    const int r = tid & (kKeys - 1);
     uint32_t tiles = 0, hc = 0;
+    TreeRing ring{SK, 0};
     while (walk.next(p, block, seg)) {
-      const TreeOrder<FP8, S> order(seg, tiles);
-      const int special0 = max(seg.i0, min(seg.i1, seg.first / kKeys));
-      for (int i = FP8 ? 0 : special0 - seg.i0; i < order.nt; ++i, ++hc) {
-        const int t = (seg.i0 + i) * kKeys + r, slot_id = hc & 1;
-        const bool live = t < seg.T;
-        const auto at = order.v(i);
-        const bool special = seg.i0 + i >= special0;
-        float ks = 0.f, vs = 0.f;
-        if constexpr (FP8) {
-          const int64_t slot = live ? tree_slot(p, seg.b, t) : -1;
-          if (slot >= 0) {
-            ks = __ldg(p.k_scale + slot * p.Hkv + seg.kvh);
-            vs = __ldg(p.v_scale + slot * p.Hkv + seg.kvh);
-          }
+      const int nt = seg.i1 - seg.i0, ahead = tree_ahead(seg);
+      for (int i = FP8 ? 0 : seg.special0 - seg.i0; i < nt; ++i, ++hc) {
+        const int t = (seg.i0 + i) * kKeys + r;
+        const uint32_t slot_id = hc % kSlots, slot_parity = hc / kSlots & 1u;
+        const bool live = t < seg.T, draft = live && t >= seg.first;
+        if (!FP8) {  // V of tile i in the one ring
+          const uint32_t at = 2 * tiles + ahead + i + min(i, nt - ahead);
+          ring.stage = at % S, ring.parity = at / S & 1u;
         }
-        wait_or_abort(v_free + slot_id, ((hc >> 1) & 1) ^ 1, abort, p.err, kErrEmptyWait);
-        if (r == 0) bad_rows[slot_id] = 0ull;
-        if constexpr (FP8) {
-          float *sc = reinterpret_cast<float *>(smem + C::oScale) + slot_id * 2 * kKeys;
-          sc[r] = ks;
-          sc[kKeys + r] = vs;
-          mbar_arrive(scale_full + slot_id);
-        }
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        if (!FP8) wait_or_abort(v_landed + slot_id, (hc >> 1) & 1, abort, p.err, kErrFullWait);
-        wait_or_abort(full + at.stage, at.parity, abort, p.err, kErrFullWait);
-        uint8_t *tile = smem + C::oStage + (size_t)at.stage * C::kTile;
-        bool clear = !live, bad = false;
-        const bool draft = live && t >= seg.first;
-        if constexpr (FP8) {
-          uint8_t *vals = smem + C::oVals + (size_t)slot_id * C::kVals;
-          if (special && draft) {
-            for (int c = 0; c < 8; ++c) {
-              uint32_t w[4];
-              lds128(w, smem_u32(tile) + r * 128 + c * 16);
+        wait_or_abort(v_free + slot_id, slot_parity ^ 1u, abort, p.err, kErrEmptyWait);
+        if (tid == 2 * 128) bad_rows[slot_id] = 0ull;
+        if (!FP8) wait_or_abort(v_landed + slot_id, slot_parity, abort, p.err, kErrFullWait);
+        wait_or_abort(full + ring.stage, ring.parity, abort, p.err, kErrFullWait);
+        uint8_t *tile = smem + C::oStage + (size_t)ring.stage * C::kTile;
+        bool bad = false;
+        if (draft) {  // whole rows
+          for (int c = 0; c < C::kPanels * 8; ++c) {
+            uint32_t w[4];
+            lds128(w, smem_u32(tile) + (c >> 3) * C::kPanel + r * 128 + (c & 7) * 16);
 #pragma unroll
-              for (int e = 0; e < 4; ++e)  // a byte of 0x7F but for the sign: NaN
+            for (int e = 0; e < 4; ++e) {
+              if constexpr (FP8)  // a byte of 0x7F but for the sign: NaN
                 bad = bad || __vcmpeq4(w[e] & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0u;
-            }
-          }
-          clear = clear || bad;
-#pragma unroll 2
-          for (int c = 0; c < 8; ++c) {
-            uint32_t w[4], o[8];
-            lds128(w, smem_u32(tile) + r * 128 + ((c ^ (r & 7)) << 4));
-#pragma unroll
-            for (int e = 0; e < 4; ++e) e4m3x4_to_bf16(clear ? 0u : w[e], o[2 * e], o[2 * e + 1]);
-            uint8_t *dst = vals + (c >> 2) * (kKeys * 128) + r * 128;
-            *reinterpret_cast<uint4 *>(dst + (((2 * c & 7) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-            *reinterpret_cast<uint4 *>(dst + (((2 * c + 1 & 7) ^ (r & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
-          }
-        } else {
-          if (draft) {
-            for (int c = 0; c < D / 8; ++c) {
-              uint32_t w[4];
-              lds128(w, smem_u32(tile) + (c >> 3) * C::kPanel + r * 128 + (c & 7) * 16);
-#pragma unroll
-              for (int e = 0; e < 4; ++e)  // an exponent of ones: infinity or NaN
+              else  // an exponent of ones: infinity or NaN
                 bad = bad || (w[e] & 0x7F80u) == 0x7F80u || (w[e] & 0x7F800000u) == 0x7F800000u;
             }
           }
-          if (clear || bad)
-            for (int c = 0; c < D / 8; ++c)
-              *reinterpret_cast<uint4 *>(tile + (c >> 3) * C::kPanel + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
         }
-        if (bad) atomicOr(reinterpret_cast<unsigned long long *>(smem + C::oBad) + slot_id, 1ull << (t - seg.first));
+        const bool clear = !live || bad;
+        if (seg.i0 + i >= seg.special0) {  // the mask is clear, and every row has been looked at
+          asm volatile("bar.sync 1, 128;" ::: "memory");
+          if (bad)
+            atomicOr(reinterpret_cast<unsigned long long *>(smem + C::oBad) + slot_id, 1ull << (t - seg.first));
+        }
+        if constexpr (FP8) {
+          uint8_t *dst0 = smem + C::oVals + (size_t)slot_id * C::kVals + r * 128;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint8_t *dst = dst0 + half * (kKeys * 128);
+            uint32_t w[4][4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) lds128(w[c], smem_u32(tile) + r * 128 + (((4 * half + c) ^ (r & 7)) << 4));
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t o[8];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) e4m3x4_to_bf16(clear ? 0u : w[c][e], o[2 * e], o[2 * e + 1]);
+              *reinterpret_cast<uint4 *>(dst + (((2 * c) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+              *reinterpret_cast<uint4 *>(dst + (((2 * c + 1) ^ (r & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+            }
+          }
+        } else if (clear) {
+          for (int c = 0; c < C::kPanels * 8; ++c)
+            *reinterpret_cast<uint4 *>(tile + (c >> 3) * C::kPanel + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+        }
         tc::fence_async_smem();
         asm volatile("bar.sync 1, 128;" ::: "memory");
-        if (r == 0) {
+        if (tid == 2 * 128) {
           mbar_arrive(v_ready + slot_id);
-          if (FP8) mbar_arrive(empty + at.stage);
+          if (FP8) mbar_arrive(empty + ring.stage);
         }
+        if (FP8) ring.next<SK, SV>();
       }
-      tiles += order.nt;
+      tiles += nt;
     }
   } else {
     regs_dec<kRegsOther>();
     if (warp == 12) {
       // ---------------------------------------------------------- loads
-      uint32_t tiles = 0;
-      const int box = p.box, nbox = kKeys / box;
+      const int box = p.box, nbox = kKeys / box, k = lane % nbox, pn = lane / nbox;  // this lane's box of a tile
+      const uint32_t to = smem_u32(smem + C::oStage) + pn * C::kPanel + k * box * 128;
+      TreeRing ring_k{0, 0}, ring_v{SK, 0};
+      auto load = [&](const CUtensorMap &map, TreeRing r, int z, int left) {  // `left` rows of the sequence
+        wait_or_abort(empty + r.stage, r.parity ^ 1u, abort, p.err, kErrEmptyWait);
+        if (__any_sync(0xffffffffu, *abort)) return;
+        const int boxes = left >= kKeys ? nbox : (left + box - 1) / box;
+        if (lane == 0) mbar_arrive_expect_tx(full + r.stage, (uint32_t)(boxes * box * 128 * C::kPanels));
+        __syncwarp();
+        if (pn < C::kPanels && k < boxes) tma_load_3d(to + r.stage * C::kTile, &map, full + r.stage, pn * (FP8 ? 128 : 64), seg.kvh, z);
+      };
+      auto load_k = [&](int z, int left) {
+        load(tmk, ring_k, z, left);
+        ring_k.next<0, SK>();
+      };
+      auto load_v = [&](int z, int left) {
+        load(tmv, FP8 ? ring_v : ring_k, z, left);
+        if (FP8) ring_v.next<SK, SV>();
+        else ring_k.next<0, SK>();
+      };
       while (walk.next(p, block, seg)) {
-        const TreeOrder<FP8, S> order(seg, tiles);
-        // lane's box of tile i: its first slot in the cache; a page outside it reads as zeros
-        auto first_slot = [&](int i) {
-          const int64_t pos = (int64_t)(seg.i0 + i) * kKeys + lane % nbox * box;
-          if (i >= order.nt || pos >= seg.T) return 0;
-          const int64_t slot = tree_slot(p, seg.b, pos);
-          return slot < 0 ? (int)p.num_slots : (int)slot;
+        const int nt = seg.i1 - seg.i0, ahead = tree_ahead(seg);
+        TreePages pages(p, seg, k * box);
+        int left = seg.T - seg.i0 * kKeys;  // rows from tile i on
+        TreePages::Row next[3] = {};        // of tiles i + ahead to i + ahead + 2: fetched before they are needed
+        int z[2] = {};                      // first slots of tiles i to i + ahead - 1; a page outside the cache reads as zeros
+        auto take = [&]() {
+          const int64_t x = TreePages::slot(p, seg, next[0]);
+          next[0] = next[1], next[1] = next[2];
+          next[2] = pages.next(p, seg.T);
+          return x < 0 ? (int)p.num_slots : (int)x;
         };
-        auto load = [&](const CUtensorMap &map, int i, int z, auto at) {
-          const uint32_t st = at.stage;
-          wait_or_abort(empty + st, at.parity ^ 1u, abort, p.err, kErrEmptyWait);
-          if (__any_sync(0xffffffffu, *abort)) return;
-          const int rows = min(kKeys, seg.T - (seg.i0 + i) * kKeys), boxes = (rows + box - 1) / box;
-          if (lane == 0) mbar_arrive_expect_tx(full + st, (uint32_t)(boxes * box * 128 * C::kPanels));
-          __syncwarp();
-          const int k = lane % nbox, pn = lane / nbox;
-          if (pn < C::kPanels && k < boxes)
-            tma_load_3d(smem_u32(smem + C::oStage + (size_t)st * C::kTile + pn * C::kPanel + k * box * 128), &map, full + st,
-                        pn * (FP8 ? 128 : 64), seg.kvh, z);
-        };
-        int z[4] = {first_slot(0), first_slot(1), first_slot(2), 0};
-        for (int i = 0; i < order.ahead; ++i) load(tmk, i, z[i], order.k(i));
-        for (int i = 0; i < order.nt; ++i) {
-          z[3] = first_slot(i + 3);  // its page number is on the way while this tile is loaded
-          load(tmv, i, z[0], order.v(i));
-          if (i + order.ahead < order.nt) load(tmk, i + order.ahead, order.ahead == 1 ? z[1] : z[2], order.k(i + order.ahead));
-          z[0] = z[1], z[1] = z[2], z[2] = z[3];
+#pragma unroll
+        for (int e = 0; e < 3; ++e) next[e] = pages.next(p, seg.T);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (e < ahead) load_k(z[e] = take(), left - e * kKeys);
+        for (int i = 0; i < nt; ++i, left -= kKeys) {
+          load_v(z[0], left);
+          const int z_new = take();
+          if (i + ahead < nt) load_k(z_new, left - ahead * kKeys);
+          z[0] = ahead == 2 ? z[1] : z_new;
+          z[1] = z_new;
         }
-        tiles += order.nt;
       }
       // Every copy has landed when the values and the products have used it; after an abort this waits for both
       // phases of every stage, as long as a copy may take.
       if (__any_sync(0xffffffffu, *abort))
         for (int st = 0; st < 2 * S; ++st) mbar_wait(full + st / 2, st & 1, kSpinLimitCycles / 100);
     } else if (warp == 13) {
-      if (lane == 0) {
       // ---------------------------------------------------------- MMA issue
+      constexpr uint32_t kTileLo = C::kTile >> 4, kPanelLo = C::kPanel >> 4, kRowsLo = kStreamRows * 128 >> 4;
+      const uint32_t one = elect_one();
       const uint32_t id_s = tc::idesc(kStreamRows, kKeys, FP8 ? 0 : 1, 0, 0), id_o = tc::idesc(kStreamRows, D, 1, 0, 1);
-      const uint32_t stage0 = smem_u32(smem + C::oStage), vals0 = smem_u32(smem + C::oVals), q0 = smem_u32(smem);
-      uint32_t tiles = 0, hc = 0, np[2] = {0, 0}, nq[2] = {0, 0};
-      auto logits = [&](int s, auto at) {  // S_s = Q_s K^T
-        const uint32_t k = stage0 + at.stage * (uint32_t)C::kTile, q = q0 + (uint32_t)(s * C::kQ);
+      const uint32_t base = smem_u32(smem), bar = smem_u32(bars), tm = uniform(tmem);
+      const uint32_t q0 = desc_lo(base, 16), k0 = desc_lo(base + (uint32_t)C::oStage, 16),
+                     v0 = desc_lo(base + (uint32_t)(FP8 ? C::oVals : C::oStage), kKeys * 128);
+      const uint32_t b_empty = bar + 8 * S, b_s = bar + 8 * (2 * S + 2), b_o = bar + 8 * (2 * S + 6), b_free = bar + 8 * (2 * S + 8 + kSlots);
+      uint32_t hc = 0;
+      TreeRing ring{0, 0};
+      uint32_t np = 0, nq = 0;  // parities of each stream's weights and queries, a bit each
+      auto flip = [](uint32_t &n, int s) {
+        const uint32_t x = n >> s & 1u;
+        n ^= 1u << s;
+        return x;
+      };
+      auto logits = [&](uint32_t s, uint32_t stage) {  // S_s = Q_s K^T
+        const uint32_t q = q0 + s * (C::kQ >> 4), k = k0 + stage * kTileLo;
         if constexpr (FP8) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            mma_e4m3(tmem + (uint32_t)(s * kKeys), tc::sdesc(q + (uint32_t)((e >> 2) * kStreamRows * 128 + (e & 3) * 32), 16, 1024, 2),
-                     tc::sdesc(k + (uint32_t)((e & 3) * 32), 16, 1024, 2), id_s, e > 0);
+          for (int e = 0; e < 8; ++e) mma_ss<true>(tm + s * kKeys, q + (e >> 2) * kRowsLo + (e & 3) * 2, k + (e & 3) * 2, id_s, e > 0, one);
         } else {
 #pragma unroll
           for (int e = 0; e < D / 16; ++e)
-            tc::mma_f16(tmem + (uint32_t)(s * kKeys), tc::sdesc(q + (uint32_t)((e >> 2) * kStreamRows * 128 + (e & 3) * 32), 16, 1024, 2),
-                        tc::sdesc(k + (uint32_t)((e >> 2) * C::kPanel + (e & 3) * 32), 16, 1024, 2), id_s, e > 0);
+            mma_ss<false>(tm + s * kKeys, q + (e >> 2) * kRowsLo + (e & 3) * 2, k + (e >> 2) * kPanelLo + (e & 3) * 2, id_s, e > 0, one);
         }
-        tc::commit(s_full + s);
+        commit_one(b_s + 8 * s, one);
       };
-      auto wait_full = [&](auto at) {
-        wait_or_abort(full + at.stage, at.parity, abort, p.err, kErrFullWait);
+      auto wait_full = [&]() {  // for the next stage of the ring
+        wait_or_abort(full + ring.stage, ring.parity, abort, p.err, kErrFullWait);
         tc::fence_after();
+        const uint32_t stage = uniform(ring.stage);
+        ring.next<0, SK>();
+        return stage;
       };
       while (walk.next(p, block, seg)) {
-        const TreeOrder<FP8, S> order(seg, tiles);
-        const int special0 = max(seg.i0, min(seg.i1, seg.first / kKeys));
-        const int streams = seg.pair ? 2 : min(2, order.nt);
-        for (int s = 0; s < streams; ++s) {
-          wait_or_abort(q_full + s, nq[s]++ & 1, abort, p.err, kErrFullWait);
-          tc::fence_after();
-          const auto at = order.k(seg.pair ? 0 : s);
-          if (!seg.pair || s == 0) wait_full(at);
-          logits(s, at);
-          if (!seg.pair || s == 1) tc::commit(empty + at.stage);
+        const int nt = seg.i1 - seg.i0, ahead = tree_ahead(seg), streams = seg.pair ? 2 : min(2, nt);
+        for (int s = 0; s < streams; ++s) wait_or_abort(q_full + s, flip(nq, s), abort, p.err, kErrFullWait);
+        tc::fence_after();
+        for (int k = 0; k < ahead; ++k) {
+          const uint32_t stage = wait_full();
+          logits(k, stage);
+          if (seg.pair) logits(1, stage);
+          commit_one(b_empty + 8 * stage, one);
         }
-        for (int i = 0; i < order.nt; ++i) {
-          const auto at = order.v(i);
-          const bool handled = FP8 || seg.i0 + i >= special0;
-          if (!FP8) wait_full(at);
+        for (int i = 0; i < nt; ++i) {
+          const bool handled = FP8 || seg.i0 + i >= seg.special0;
+          const uint32_t slot = uniform(hc % kSlots), stage = FP8 ? 0 : wait_full();
           if (handled) {
-            if (!FP8) mbar_arrive(v_landed + (hc & 1));
-            wait_or_abort(v_ready + (hc & 1), (hc >> 1) & 1, abort, p.err, kErrFullWait);
+            if (!FP8 && lane == 0) mbar_arrive(v_landed + slot);
+            wait_or_abort(v_ready + slot, hc / kSlots & 1u, abort, p.err, kErrFullWait);
             tc::fence_after();
           }
-          const uint32_t v = FP8 ? vals0 + (hc & 1) * (uint32_t)C::kVals : stage0 + at.stage * (uint32_t)C::kTile;
-          const int s0 = seg.pair ? 0 : i & 1, s1 = seg.pair ? 1 : s0;
-          for (int s = s0; s <= s1; ++s) {
-            wait_or_abort(p_full + s, np[s]++ & 1, abort, p.err, kErrFullWait);
+          const uint32_t v = v0 + (FP8 ? slot * (C::kVals >> 4) : stage * kTileLo);
+          uint32_t next = 0;
+          auto product = [&](uint32_t s, bool first, bool last) {  // O_s += P_s V, then the logits of the stream's next tile
+            wait_or_abort(p_full + s, flip(np, s), abort, p.err, kErrFullWait);
             tc::fence_after();
 #pragma unroll
-            for (int e = 0; e < kKeys / 16; ++e)  // O_s += P_s V
-              mma_ts_f16(tmem + 256u + (uint32_t)(s * D), tmem + (uint32_t)(s * kKeys + e * 8),
-                         tc::sdesc(v + (uint32_t)e * 2048u, kKeys * 128, 1024, 2), id_o);
-            tc::commit(o_full + s);
-            if (s == s1) {
-              if (!FP8) tc::commit(empty + at.stage);
-              if (handled) tc::commit(v_free + (hc & 1));
+            for (int e = 0; e < kKeys / 16; ++e)
+              mma_ts_f16(tm + 256u + s * D, tm + s * kKeys + (uint32_t)(e * 8), v + e * (2048u >> 4), id_o, one);
+            commit_one(b_o + 8 * s, one);
+            if (last && !FP8) commit_one(b_empty + 8 * stage, one);
+            if (last && handled) commit_one(b_free + 8 * slot, one);
+            if (i + ahead < nt) {
+              if (first) next = wait_full();
+              logits(s, next);
+              if (last) commit_one(b_empty + 8 * next, one);
             }
-            const int k = i + (seg.pair ? 1 : 2);  // this stream's next tile
-            if (k < order.nt) {
-              if (s == s0) wait_full(order.k(k));
-              logits(s, order.k(k));
-              if (s == s1) tc::commit(empty + order.k(k).stage);
-            }
+          };
+          if (seg.pair) {
+            product(0, true, false);
+            product(1, false, true);
+          } else {
+            product(uniform(i & 1), true, true);
           }
           hc += handled;
         }
-        tiles += order.nt;
       }
-      tc::commit(done);
+      commit_one(smem_u32(done), one);
       mbar_wait(done, 0);  // no product in flight when the tensor memory is freed
+    } else if (FP8 && warp == 14) {
+      // ---------------------------------------------------------- scales
+      float *sc = reinterpret_cast<float *>(smem + C::oScale);
+      uint32_t hc = 0;
+      while (walk.next(p, block, seg)) {
+        const int nt = seg.i1 - seg.i0;
+        TreePages pages[4] = {TreePages(p, seg, lane), TreePages(p, seg, lane + 32), TreePages(p, seg, lane + 64), TreePages(p, seg, lane + 96)};
+        TreePages::Row next[4][2];  // of tiles i and i + 1
+#pragma unroll
+        for (int k = 0; k < 4; ++k) next[k][0] = pages[k].next(p, seg.T), next[k][1] = pages[k].next(p, seg.T);
+        for (int i = 0; i < nt; ++i, ++hc) {
+          const uint32_t slot_id = hc % kSlots;
+          wait_or_abort(v_free + slot_id, (hc / kSlots & 1u) ^ 1u, abort, p.err, kErrEmptyWait);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {  // rows that are not there get 0
+            const int64_t at = TreePages::slot(p, seg, next[k][0]);
+            const uint32_t dst = smem_u32(sc + slot_id * 2 * kKeys + 32 * k + lane), bytes = at >= 0 ? 4u : 0u;
+            const int64_t e = at >= 0 ? at * p.Hkv + seg.kvh : 0;
+            cp_async_4_or_zero(dst, p.k_scale + e, bytes);
+            cp_async_4_or_zero(dst + kKeys * 4, p.v_scale + e, bytes);
+            next[k][0] = next[k][1];
+            next[k][1] = pages[k].next(p, seg.T);
+          }
+          cp_async_mbar_arrive_noinc(scale_full + slot_id);
+        }
       }
-      __syncwarp();
+      cp_async_wait_all();
     }
   }
   tc::fence_before();

@@ -217,6 +217,17 @@ def test_tree_attn_long_context_splits():
     check(out, want, bound, ~want.isnan())
 
 
+@pytest.mark.parametrize("dtype,G,N", [("bf16", 8, 5), ("e4m3", 8, 16), ("bf16", 8, 33), ("e4m3", 16, 20)])
+def test_tree_attn_many_units_per_share(dtype, G, N):
+    """A large batch of short sequences: shares that hold several whole units of several tiles, and cut ones."""
+    lens = [300 + 37 * i % 411 for i in range(60)] + [0, 20000]
+    c, q, masks, words = tree_case(dtype, 4, G, 128, 32, N, lens, [N] * len(lens), seed=10)
+    out = torch.full_like(q, 77.0)
+    hs2.tree_attn(q, c.k, c.v, c.lens, tree_mask=words, out=out, **c.kw())
+    want, bound = R.tree_reference(c, q, [N] * len(lens), masks, dtype)
+    check(out, want, bound, ~want.isnan())
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
 def test_tree_attn_growing_and_large_logits(dtype):
     """Logits that grow along the context by hundreds of nats (the running maximum moves at every tile), and shrink."""
