@@ -13,9 +13,12 @@
 // other tile, so a memory-bound call has two warpgroups at work, too; their sums
 // are joined at the end.
 //
-// m moves only when a row's maximum passes it by more than 8 (in base-2
-// exponents): weights stay below 2^8, which bf16 and fp32 sums hold as well as
-// weights below 1, and O_s is rescaled a few times per unit instead of per tile.
+// A stream works on 64 columns at a time, so the first half's product is under way
+// during the second half's exponentials.  m is the maximum of a row's first columns
+// and moves only when later weights pass it far (their sum over 64 columns passes
+// 2^15): weights that stay below need no maximum, so an ordinary tile is read from
+// tensor memory once, and O_s is rescaled a few times per unit instead of per tile.
+// bf16 and fp32 sums hold such weights as well as weights below 1.
 //
 // E4M3 caches.  S_s uses the codes as they are: the query row, scaled by a power
 // of two to at most 448, is split into two E4M3 terms hi + lo (a bf16 value has
@@ -26,7 +29,7 @@
 // by a warpgroup of its own, and its scale joins the weight before it is rounded.
 //
 // Roles: warps 0-3 and 4-7 the streams, 8-11 the values (conversion, and rows
-// that must not be multiplied, below), 12 the TMA loads, 13 the MMA issue, 14 E4M3's scales.
+// that must not be multiplied, below), 12 the TMA loads, 13 the MMA issue, 14-15 E4M3's scales.
 //
 // Rows of V that a query row must not see, whatever they hold: weight 0 times
 // NaN is NaN in a matrix product, so the values warpgroup clears the rows behind
@@ -47,9 +50,9 @@ constexpr int kKeys = 128;       // positions per tile
 constexpr int kStreamRows = 128;
 constexpr int kThreads = 512;
 constexpr int kTmemCols = 512;
-// 65,536 registers: 2 x 128 threads x 200 and 2 x 128 x 56
-constexpr int kRegsStream = 200, kRegsOther = 56;
-constexpr float kMaxGrowth = 8.f;
+// 65,536 registers: 2 x 128 threads x 176 and 2 x 128 x 80
+constexpr int kRegsStream = 176, kRegsOther = 80;
+constexpr float kMaxGrowth = 8.f, kMaxSum = 32768.f;
 
 template <int D, bool FP8>
 struct TreeTc {
@@ -63,8 +66,9 @@ struct TreeTc {
   static constexpr int kSlots = 2;  // tiles in the values warpgroup's hands
   static constexpr size_t oStage = 2 * kQ, oVals = oStage + (size_t)kStages * kTile, oScale = oVals + kSlots * kVals,
                           oBar = oScale + (FP8 ? kSlots * 2 * kKeys * 4 : 0);
-  // full[S], empty[S], q_full[2], s_full[2], p_full[2], o_full[2], and per slot v_ready, v_free, scale_full, v_landed; done
-  static constexpr int kBars = 2 * kStages + 8 + 4 * kSlots + 1;
+  // p_full and o_full: a stream's halves of a tile
+  // full[S], empty[S], q_full[2], s_full[2], p_full[2][2], o_full[2][2], and per slot v_ready, v_free, scale_full, v_landed; done
+  static constexpr int kBars = 2 * kStages + 12 + 4 * kSlots + 1;
   static constexpr size_t oBad = oBar + (size_t)((kBars * 8 + 15) / 16 * 16), oInfo = oBad + 8 * kSlots, kBytes = oInfo + 64 + 1024;
   static_assert(kBytes <= 232448, "shared memory of a CTA");
 };
@@ -79,7 +83,7 @@ struct TreeInfo {  // shared
 // One unit's part in a share.
 struct TreeSeg {
   int b, kvh, i0, i1, T, first, nr, special0;  // special0: the first tile with a draft, or rows behind the sequence
-  bool pair, begins, whole;
+  bool pair, few, begins, whole;  // few: at most 64 rows
 };
 
 // Tiles are numbered in 32 bits: the entry points keep them below 2^31.
@@ -108,6 +112,7 @@ struct TreeWalk {
       g += s.i1 - s.i0;
       s.nr = min(2 * kStreamRows, n * p.G - block * 2 * kStreamRows);
       s.pair = s.nr > kStreamRows;
+      s.few = s.nr <= kStreamRows / 2;
       if (s.nr > 0) return true;
     }
     return false;
@@ -193,6 +198,12 @@ __device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
 // 4 bytes, or zeros with bytes = 0
 __device__ __forceinline__ void cp_async_4_or_zero(uint32_t dst, const void *src, uint32_t bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+// shared loads that stay where they are written
+__device__ __forceinline__ float2 lds_float2(const float *p) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(smem_u32(p)));
+  return v;
 }
 // 64 columns
 __device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
@@ -325,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::oBar);
   constexpr int kSlots = C::kSlots, SK = C::kStagesK, SV = C::kStagesV;
   uint64_t *full = bars, *empty = bars + S, *q_full = bars + 2 * S, *s_full = q_full + 2, *p_full = q_full + 4,
-           *o_full = q_full + 6, *v_ready = q_full + 8, *v_free = v_ready + kSlots, *scale_full = v_free + kSlots,
+           *o_full = q_full + 8, *v_ready = q_full + 12, *v_free = v_ready + kSlots, *scale_full = v_free + kSlots,
            *v_landed = scale_full + kSlots, *done = v_landed + kSlots;
   volatile uint64_t *bad_rows = reinterpret_cast<volatile uint64_t *>(smem + C::oBad);
   TreeInfo *info = reinterpret_cast<TreeInfo *>(smem + C::oInfo);
@@ -337,9 +348,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < C::kBars; ++i) mbar_init(bars + i, 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(q_full + s, 4);
-      mbar_init(p_full + s, 4);
+      mbar_init(p_full + 2 * s, 4);
+      mbar_init(p_full + 2 * s + 1, 4);
     }
-    for (int s = 0; s < kSlots; ++s) mbar_init(scale_full + s, 32);
+    for (int s = 0; s < kSlots; ++s) mbar_init(scale_full + s, 64);
     fence_mbar_init();
     info->abort = 0;
     info->g0 = info->g1 = 0;
@@ -401,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (wg < 2) {
     // ------------------------------------------------------------ a stream
     regs_inc<kRegsStream>();
-    const int s = wg, row = tid & 127;
+    const int s = wg;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
     const uint32_t ts = tmem + lanes + (uint32_t)(s * kKeys), to = tmem + lanes + 256u + (uint32_t)(s * D);
     uint8_t *sq = smem + s * C::kQ;
@@ -414,9 +426,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         handled0 += handled_here;
         continue;
       }
+      // with M = 64 the product leaves 16 rows in the first half of each warp's lanes
+      const int row = seg.few ? (warp & 3) * 16 + (lane & 15) : tid & 127;
       const int r = block * 2 * kStreamRows + (seg.pair ? s * kStreamRows : 0) + row;
       const int n = seg.T - seg.first;
-      const bool mine = r < n * p.G, busy = __any_sync(0xffffffffu, mine);
+      const bool mine = r < n * p.G && !(seg.few && lane >= 16), busy = __any_sync(0xffffffffu, mine);
       const int tok = r / p.G, head = seg.kvh * p.G + r % p.G;
       const uint64_t bits = mine ? tree_bits(p, seg.b, tok, n) : 0ull;
       float c2 = p.c2;
@@ -483,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
       const float growth = kMaxGrowth / c2;
       float m = -INFINITY, l = 0.f;
-      bool first_tile = true;
+      bool any_product = false;  // whether O holds a product
       for (int i = seg.pair ? 0 : s; i < nt; i += seg.pair ? 1 : 2) {
         const int t0 = (seg.i0 + i) * kKeys;
         const bool special = seg.i0 + i >= seg.special0;
@@ -493,126 +507,144 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::fence_after();
         if (FP8) wait_or_abort(scale_full + slot_id, slot_parity, abort, p.err, kErrFullWait);
         if (special) wait_or_abort(v_ready + slot_id, slot_parity, abort, p.err, kErrFullWait);
-        if (busy) {
-          float x[2][64];
-          tmem_ld64(ts, x[0]);
-          tmem_ld64(ts + 64, x[1]);
-          const float *ks = reinterpret_cast<const float *>(smem + C::oScale) + slot_id * 2 * kKeys, *vs = ks + kKeys;
-          if constexpr (FP8) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-              for (int e = 0; e < 64; e += 4) {
-                const float4 f = *reinterpret_cast<const float4 *>(ks + 64 * h + e);
-                const float2 u = mul2(make_float2(x[h][e], x[h][e + 1]), make_float2(f.x, f.y));
-                const float2 w = mul2(make_float2(x[h][e + 2], x[h][e + 3]), make_float2(f.z, f.w));
-                x[h][e] = u.x, x[h][e + 1] = u.y, x[h][e + 2] = w.x, x[h][e + 3] = w.y;
-              }
-          }
-          uint64_t seen[2] = {~0ull, ~0ull};
-          if (special) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int rel = seg.first - t0 - 64 * h;
-              seen[h] = below(rel) | shift_bits(bits, rel);
-              const uint32_t lo = (uint32_t)seen[h], hi = (uint32_t)(seen[h] >> 32);
-#pragma unroll
-              for (int e = 0; e < 64; ++e)
-                if (!(((e < 32 ? lo : hi) >> (e & 31)) & 1u)) x[h][e] = -INFINITY;
-            }
-          }
-          float mx[8];
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            mx[c] = fmaxf(x[0][c], x[1][c]);
-#pragma unroll
-            for (int e = 8; e < 64; e += 8) mx[c] = fmaxf(fmaxf(mx[c], x[0][c + e]), x[1][c + e]);
-          }
-          const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
-          const bool grow = m == -INFINITY ? top > -INFINITY : top > m + growth;
-          const uint64_t bad = special ? bad_rows[slot_id] : 0ull;
-          if (__any_sync(0xffffffffu, grow) || bad) {
-            float alpha = 1.f;
-            if (grow) {
-              alpha = m == -INFINITY ? 0.f : ex2_approx((m - top) * c2);
-              m = top;
-              l *= alpha;
-            }
-            __syncwarp();
-            if (!first_tile) {
-              wait_or_abort(o_full + s, (ns - 1) & 1u, abort, p.err, kErrFullWait);  // the last product is in O
-              tc::fence_after();
+        const float *ks = reinterpret_cast<const float *>(smem + C::oScale) + slot_id * 2 * kKeys, *vs = ks + kKeys;
+        const uint64_t bad = special ? bad_rows[slot_id] : 0ull;
 #pragma unroll 1
-              for (int c = 0; c < D; c += 32) {
-                float o[32];
-                tc::ld32(to + c, o);
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t tx = ts + 64 * h;  // this half's logits, and its weights over them
+          // O after the last product, times alpha
+          auto rescale = [&](float alpha) {
+            wait_or_abort(o_full + 2 * s + (h ^ 1), (h ? ns : ns - 1) & 1u, abort, p.err, kErrFullWait);
+            tc::fence_after();
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              float o[32];
+              tc::ld32(to + c, o);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] *= alpha;
-                tc::st32(to + c, o);
-              }
+              for (int e = 0; e < 32; ++e) o[e] *= alpha;
+              tc::st32(to + c, o);
             }
-          }
-          const float shift = m == -INFINITY ? 0.f : -m * c2;  // nothing seen yet: weights 0
-          float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
-          const float2 cc = make_float2(c2, c2), sh = make_float2(shift, shift);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
+          };
+          if (busy) {
+            uint64_t bad_here = 0;
             uint32_t w[32];
+            float sum;
+            bool look = special || __any_sync(0xffffffffu, mine && m == -INFINITY);
+            if (!look) {  // all is seen, and m is near
+              const float2 cc = make_float2(c2, c2), sh = make_float2(-m * c2, -m * c2);
+              float x[64];
+              float2 sums[2] = {{0.f, 0.f}, {0.f, 0.f}};
+              tmem_ld64(tx, x);
 #pragma unroll
-            for (int e = 0; e < 64; e += 2) {
-              float2 a = fma2(make_float2(x[h][e], x[h][e + 1]), cc, sh);
-              a.x = ex2_approx(a.x), a.y = ex2_approx(a.y);
-              sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], a);
-              if constexpr (FP8) {
-                a = mul2(a, *reinterpret_cast<const float2 *>(vs + 64 * h + e));
-                if (special) {  // a scale that is not seen may be anything
-                  a.x = (seen[h] >> e) & 1ull ? a.x : 0.f;
-                  a.y = (seen[h] >> (e + 1)) & 1ull ? a.y : 0.f;
-                }
+              for (int e = 0; e < 64; e += 2) {
+                float2 a = make_float2(x[e], x[e + 1]), kc = cc;
+                if constexpr (FP8) kc = mul2(cc, lds_float2(ks + 64 * h + e));
+                a = fma2(a, kc, sh);
+                a.x = ex2_approx(a.x), a.y = ex2_approx(a.y);
+                sums[(e >> 1) & 1] = add2(sums[(e >> 1) & 1], a);
+                if constexpr (FP8) a = mul2(a, lds_float2(vs + 64 * h + e));
+                w[e >> 1] = pack_bf16(a.x, a.y);
               }
-              w[e >> 1] = pack_bf16(a.x, a.y);
+              const float2 both = add2(sums[0], sums[1]);
+              sum = both.x + both.y;
+              look = __any_sync(0xffffffffu, mine && sum > kMaxSum);
             }
-            tmem_st32(ts + 32 * h, w);
-          }
-          tmem_wait_st();
-          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-          if (bad) {  // rare: drafts whose values are not finite, for the rows that see them
-            for (uint64_t rest = bad; rest; rest &= rest - 1) {
-              const int j = __ffsll((long long)rest) - 1, c = seg.first + j - t0;
-              const uint32_t pw = tmem_ld1(ts + (c >> 1));
-              const float w = c & 1 ? bf16_hi(pw) : bf16_lo(pw);
-              const bool sees = (bits >> j) & 1ull;
-              const int64_t slot = tree_slot(p, seg.b, seg.first + j);
-              const int64_t at = (slot * p.Hkv + seg.kvh) * D;
-              if (slot < 0) continue;  // the same for the warp
-#pragma unroll 1
-              for (int d = 0; d < D; d += 32) {
-                float o[32];
-                tc::ld32(to + d, o);
+            if (look) {
+              const int j0 = t0 + 64 * h - seg.first;  // the draft in the half's first column
+              const uint64_t seen = special ? below(-j0) | shift_bits(bits, -j0) : ~0ull;
+              bad_here = bad & ~below(j0) & below(j0 + 64);
+              // 32 logits from column c of the half on, times the keys' scales, the hidden ones at -infinity
+              auto load_logits = [&](int c, float(&x)[32]) {
+                tc::ld32(tx + c, x);
+                if constexpr (FP8) {
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                  float v;
-                  if constexpr (FP8) {
-                    const __half_raw hr = __nv_cvt_fp8_to_halfraw(static_cast<const uint8_t *>(p.v)[at + d + e], __NV_E4M3);
-                    v = __half2float(*reinterpret_cast<const __half *>(&hr));
-                  } else {
-                    v = __bfloat162float(static_cast<const __nv_bfloat16 *>(p.v)[at + d + e]);
+                  for (int e = 0; e < 32; e += 2) {
+                    const float2 u = mul2(make_float2(x[e], x[e + 1]), lds_float2(ks + 64 * h + c + e));
+                    x[e] = u.x, x[e + 1] = u.y;
                   }
-                  if (sees) o[e] = fmaf(w, v, o[e]);
                 }
-                tc::st32(to + d, o);
+                const uint32_t see = (uint32_t)(seen >> c);
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if (!((see >> e) & 1u)) x[e] = -INFINITY;
+              };
+              float top = -INFINITY;
+#pragma unroll
+              for (int c = 0; c < 64; c += 32) {
+                float x[32];
+                load_logits(c, x);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) top = fmaxf(top, x[e]);
+              }
+              float alpha = 1.f;
+              if (m == -INFINITY ? top > -INFINITY : top > m + growth) {
+                alpha = m == -INFINITY ? 0.f : ex2_approx((m - top) * c2);
+                m = top;
+                l *= alpha;
+              }
+              __syncwarp();
+              if (any_product && (bad_here || __any_sync(0xffffffffu, alpha != 1.f))) rescale(alpha);
+              const float shift = m == -INFINITY ? 0.f : -m * c2;  // nothing seen yet: weights 0
+              sum = 0.f;
+#pragma unroll
+              for (int c = 0; c < 64; c += 32) {
+                float x[32];
+                load_logits(c, x);
+                const uint32_t see = (uint32_t)(seen >> c);
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                  float2 a = make_float2(ex2_approx(fmaf(x[e], c2, shift)), ex2_approx(fmaf(x[e + 1], c2, shift)));
+                  sum += a.x + a.y;
+                  if constexpr (FP8) {  // a scale that is not seen may be anything
+                    a = mul2(a, lds_float2(vs + 64 * h + c + e));
+                    a.x = (see >> e) & 1u ? a.x : 0.f;
+                    a.y = (see >> (e + 1)) & 1u ? a.y : 0.f;
+                  }
+                  w[(c + e) >> 1] = pack_bf16(a.x, a.y);
+                }
               }
             }
+            l += sum;
+            tmem_st32(tx, w);
+            tmem_wait_st();
+            if (bad_here) {  // rare: drafts whose values are not finite, for the rows that see them
+              for (uint64_t rest = bad_here; rest; rest &= rest - 1) {
+                const int j = __ffsll((long long)rest) - 1, c = seg.first + j - t0 - 64 * h;
+                const uint32_t pw = tmem_ld1(tx + (c >> 1));
+                const float wj = c & 1 ? bf16_hi(pw) : bf16_lo(pw);
+                const bool sees = (bits >> j) & 1ull;
+                const int64_t slot = tree_slot(p, seg.b, seg.first + j);
+                if (slot < 0) continue;  // the same for the warp
+                const int64_t at = (slot * p.Hkv + seg.kvh) * D;
+#pragma unroll 1
+                for (int d = 0; d < D; d += 32) {
+                  float o[32];
+                  tc::ld32(to + d, o);
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) {
+                    float v;
+                    if constexpr (FP8) {
+                      const __half_raw hr = __nv_cvt_fp8_to_halfraw(static_cast<const uint8_t *>(p.v)[at + d + e], __NV_E4M3);
+                      v = __half2float(*reinterpret_cast<const __half *>(&hr));
+                    } else {
+                      v = __bfloat162float(static_cast<const __nv_bfloat16 *>(p.v)[at + d + e]);
+                    }
+                    if (sees) o[e] = fmaf(wj, v, o[e]);
+                  }
+                  tc::st32(to + d, o);
+                }
+              }
+            }
+            tc::fence_before();
           }
-          tc::fence_before();
+          any_product = true;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full + 2 * s + h);
         }
-        first_tile = false;
         ++ns;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full + s);
       }
       handled0 += handled_here;
-      wait_or_abort(o_full + s, (ns - 1) & 1u, abort, p.err, kErrFullWait);
+      wait_or_abort(o_full + 2 * s + 1, (ns - 1) & 1u, abort, p.err, kErrFullWait);
       tc::fence_after();
       // A unit inside the share is finished here, by stream 0: of a unit whose tiles both streams took, stream 1 hands
       // its sums over in a record of their own, which stream 0 has read before stream 1 writes the next.
@@ -807,11 +839,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------------------- MMA issue
       constexpr uint32_t kTileLo = C::kTile >> 4, kPanelLo = C::kPanel >> 4, kRowsLo = kStreamRows * 128 >> 4;
       const uint32_t one = elect_one();
-      const uint32_t id_s = tc::idesc(kStreamRows, kKeys, FP8 ? 0 : 1, 0, 0), id_o = tc::idesc(kStreamRows, D, 1, 0, 1);
+      const uint32_t id_s128 = tc::idesc(kStreamRows, kKeys, FP8 ? 0 : 1, 0, 0), id_o128 = tc::idesc(kStreamRows, D, 1, 0, 1);
+      const uint32_t id_s64 = tc::idesc(kStreamRows / 2, kKeys, FP8 ? 0 : 1, 0, 0), id_o64 = tc::idesc(kStreamRows / 2, D, 1, 0, 1);
+      uint32_t id_s = id_s128, id_o = id_o128;
       const uint32_t base = smem_u32(smem), bar = smem_u32(bars), tm = uniform(tmem);
       const uint32_t q0 = desc_lo(base, 16), k0 = desc_lo(base + (uint32_t)C::oStage, 16),
                      v0 = desc_lo(base + (uint32_t)(FP8 ? C::oVals : C::oStage), kKeys * 128);
-      const uint32_t b_empty = bar + 8 * S, b_s = bar + 8 * (2 * S + 2), b_o = bar + 8 * (2 * S + 6), b_free = bar + 8 * (2 * S + 8 + kSlots);
+      const uint32_t b_empty = bar + 8 * S, b_s = bar + 8 * (2 * S + 2), b_o = bar + 8 * (2 * S + 8), b_free = bar + 8 * (2 * S + 12 + kSlots);
       uint32_t hc = 0;
       TreeRing ring{0, 0};
       uint32_t np = 0, nq = 0;  // parities of each stream's weights and queries, a bit each
@@ -841,6 +875,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       while (walk.next(p, block, seg)) {
         const int nt = seg.i1 - seg.i0, ahead = tree_ahead(seg), streams = seg.pair ? 2 : min(2, nt);
+        id_s = uniform(seg.few ? id_s64 : id_s128), id_o = uniform(seg.few ? id_o64 : id_o128);
         for (int s = 0; s < streams; ++s) wait_or_abort(q_full + s, flip(nq, s), abort, p.err, kErrFullWait);
         tc::fence_after();
         for (int k = 0; k < ahead; ++k) {
@@ -860,12 +895,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t v = v0 + (FP8 ? slot * (C::kVals >> 4) : stage * kTileLo);
           uint32_t next = 0;
           auto product = [&](uint32_t s, bool first, bool last) {  // O_s += P_s V, then the logits of the stream's next tile
-            wait_or_abort(p_full + s, flip(np, s), abort, p.err, kErrFullWait);
-            tc::fence_after();
+            const uint32_t parity = flip(np, s);
 #pragma unroll
-            for (int e = 0; e < kKeys / 16; ++e)
-              mma_ts_f16(tm + 256u + s * D, tm + s * kKeys + (uint32_t)(e * 8), v + e * (2048u >> 4), id_o, one);
-            commit_one(b_o + 8 * s, one);
+            for (int h = 0; h < 2; ++h) {
+              wait_or_abort(p_full + 2 * s + h, parity, abort, p.err, kErrFullWait);
+              tc::fence_after();
+#pragma unroll
+              for (int e = 0; e < kKeys / 32; ++e)
+                mma_ts_f16(tm + 256u + s * D, tm + s * kKeys + (uint32_t)(h * 64 + e * 8), v + (h * 4 + e) * (2048u >> 4), id_o, one);
+              commit_one(b_o + 8 * (2 * s + h), one);
+            }
             if (last && !FP8) commit_one(b_empty + 8 * stage, one);
             if (last && handled) commit_one(b_free + 8 * slot, one);
             if (i + ahead < nt) {
@@ -885,23 +924,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       commit_one(smem_u32(done), one);
       mbar_wait(done, 0);  // no product in flight when the tensor memory is freed
-    } else if (FP8 && warp == 14) {
+    } else if (FP8 && warp >= 14) {
       // ---------------------------------------------------------- scales
       float *sc = reinterpret_cast<float *>(smem + C::oScale);
       uint32_t hc = 0;
       while (walk.next(p, block, seg)) {
         const int nt = seg.i1 - seg.i0;
-        TreePages pages[4] = {TreePages(p, seg, lane), TreePages(p, seg, lane + 32), TreePages(p, seg, lane + 64), TreePages(p, seg, lane + 96)};
-        TreePages::Row next[4][2];  // of tiles i and i + 1
+        const int r0 = (warp - 14) * 64 + lane;  // and the row 32 further
+        TreePages pages[2] = {TreePages(p, seg, r0), TreePages(p, seg, r0 + 32)};
+        TreePages::Row next[2][2];  // of tiles i and i + 1
 #pragma unroll
-        for (int k = 0; k < 4; ++k) next[k][0] = pages[k].next(p, seg.T), next[k][1] = pages[k].next(p, seg.T);
+        for (int k = 0; k < 2; ++k) next[k][0] = pages[k].next(p, seg.T), next[k][1] = pages[k].next(p, seg.T);
         for (int i = 0; i < nt; ++i, ++hc) {
           const uint32_t slot_id = hc % kSlots;
           wait_or_abort(v_free + slot_id, (hc / kSlots & 1u) ^ 1u, abort, p.err, kErrEmptyWait);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {  // rows that are not there get 0
+          for (int k = 0; k < 2; ++k) {  // rows that are not there get 0
             const int64_t at = TreePages::slot(p, seg, next[k][0]);
-            const uint32_t dst = smem_u32(sc + slot_id * 2 * kKeys + 32 * k + lane), bytes = at >= 0 ? 4u : 0u;
+            const uint32_t dst = smem_u32(sc + slot_id * 2 * kKeys + r0 + 32 * k), bytes = at >= 0 ? 4u : 0u;
             const int64_t e = at >= 0 ? at * p.Hkv + seg.kvh : 0;
             cp_async_4_or_zero(dst, p.k_scale + e, bytes);
             cp_async_4_or_zero(dst + kKeys * 4, p.v_scale + e, bytes);
