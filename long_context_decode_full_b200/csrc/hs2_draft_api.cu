@@ -38,12 +38,17 @@ struct TreePlan {
   size_t prefix, records, total;
 };
 
-TreePlan tree_plan(int B, int N, int G, int D, bool f32) {
+// t_cap: the capacity per sequence (fp32 caches: short tiles where long ones are too few)
+TreePlan tree_plan(int B, int N, int Hkv, int G, int D, bool f32, int64_t t_cap) {
   TreePlan t{};
-  t.tile = f32 ? tree_f32_tile() : tree_tc_tile();
-  t.rows = f32 ? tree_f32_rows() : tree_tc_rows();
+  t.tile = tree_tc_tile();
+  t.rows = tree_tc_rows();
   t.streams = f32 ? 1 : 2;
-  const int ctas = sm_count() * (f32 ? tree_f32_ctas_per_sm(D) : 1), per_block = t.rows * t.streams;
+  if (f32) {
+    t.rows = N * G <= 32 ? 32 : 64;
+    t.tile = t.rows == 32 && (t_cap + 63) / 64 * Hkv * B < sm_count() ? 32 : 64;
+  }
+  const int ctas = sm_count() * (f32 ? tree_f32_ctas_per_sm(D, t.rows, t.tile) : 1), per_block = t.rows * t.streams;
   t.blocks = (N * G + per_block - 1) / per_block;
   t.groups = ctas / t.blocks < 1 ? 1 : (ctas / t.blocks > kMaxTreeGroups ? kMaxTreeGroups : ctas / t.blocks);
   t.prefix = 256;
@@ -171,7 +176,11 @@ size_t hs2_tree_attn_workspace(int32_t batch, int32_t tokens, int32_t num_kv_hea
   if (batch < 1 || batch > kMaxBatchSmem || tokens < 1 || tokens > kMaxDraft || num_kv_heads < 1 || !group_ok(group) ||
       (head_dim != 64 && head_dim != 128) || kv_dtype < HS2_F32 || kv_dtype > HS2_E4M3)
     return 0;
-  return tree_plan(batch, tokens, group, head_dim, kv_dtype == HS2_F32).total;
+  // the larger of the plans that the call may choose by its capacity
+  const bool f32 = kv_dtype == HS2_F32;
+  const size_t a = tree_plan(batch, tokens, num_kv_heads, group, head_dim, f32, 1).total;
+  const size_t b = tree_plan(batch, tokens, num_kv_heads, group, head_dim, f32, kMaxContext).total;
+  return a > b ? a : b;
 }
 
 int hs2_tree_attn(const hs2_tokens *q, const hs2_cache *k_cache, const hs2_cache *v_cache, const int32_t *seq_lens,
@@ -198,7 +207,7 @@ int hs2_tree_attn(const hs2_tokens *q, const hs2_cache *k_cache, const hs2_cache
   if (k_cache->dtype != HS2_F32 && page_table && !(ps % 16 == 0 && (ps % 64 == 0 || 64 % ps == 0)))
     return fail(HS2_ERR_UNSUPPORTED, "page_size %d (16, 32 or a multiple of 64)", ps);
   const bool f32 = k_cache->dtype == HS2_F32;
-  const TreePlan plan = tree_plan(q->batch, q->tokens, G, D, f32);
+  const TreePlan plan = tree_plan(q->batch, q->tokens, Hkv, G, D, f32, t_cap);
   if (!workspace) return fail(HS2_ERR_WORKSPACE, "workspace is NULL");
   if (reinterpret_cast<uintptr_t>(workspace) & 255) return fail(HS2_ERR_WORKSPACE, "workspace not 256-byte aligned");
   if (workspace_bytes < plan.total)

@@ -98,13 +98,15 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_kernel(const AcceptPara
 // The kept positions of a unit (sequence, kv head) over its budget K: of the
 // positions below T - W the K - W with the largest sums (ties to the lower
 // position, NaN below everything), then the window.  A cluster of CTAs per unit
-// takes equal shares of the positions: three radix passes (11, 11, 10 bits of
-// an order-preserving key; histograms in shared memory, added over the cluster
-// through distributed shared memory) find the exact key of the last one taken,
-// then each share writes its positions behind the earlier shares' counts.
-// Bound by reading the sums four times from L2 and by nine cluster barriers.
-constexpr int kPickThreads = 512;
+// takes equal shares of the positions: three radix passes (11, 11, 10 bits of an
+// order-preserving key) find the exact key of the last one taken, then each share
+// writes its positions behind the earlier shares' counts.  A pass counts into shared
+// memory; each CTA adds its part of the bins over the cluster and hands the sums to
+// all (distributed shared memory), so every CTA finds the bin itself.  A share's
+// keys stay in registers where they fit.  Bound by seven cluster barriers.
+constexpr int kPickThreads = 1024;
 constexpr int kPickBins = 2048;
+constexpr int kPickKeys = 16;  // of a thread, in registers
 
 __device__ __forceinline__ uint32_t sum_key(float x) {
   const uint32_t u = __float_as_uint(x);
@@ -115,8 +117,8 @@ __device__ __forceinline__ uint32_t sum_key(float x) {
 
 __global__ void __launch_bounds__(kPickThreads) pick_kernel(const EvictParams p) {
   __shared__ uint32_t sh_hist[kPickBins], sh_tot[kPickBins];
-  __shared__ int sh_warp[33], sh_res[2], sh_found[2];
-  __shared__ int2 sh_counts[16];
+  __shared__ int sh_warp[33], sh_res[2];
+  __shared__ int2 sh_counts[8];
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   griddep_wait();
@@ -135,6 +137,15 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const EvictParams p)
   for (int i = rank * kPickThreads + tid; i < W; i += C * kPickThreads) kept[take + i] = n + i;
   if (take == 0) return;
   const int share = (n + C - 1) / C, c0 = min(n, rank * share), c1 = min(n, c0 + share);
+  const bool held = share <= kPickKeys * kPickThreads;
+  uint32_t keys[kPickKeys];
+  if (held) {
+#pragma unroll
+    for (int k = 0; k < kPickKeys; ++k) {
+      const int t = c0 + k * kPickThreads + tid;
+      keys[k] = t < c1 ? sum_key(__ldg(acc + t)) : 0u;
+    }
+  }
   uint32_t prefix = 0;
   int need = take;
   for (int pass = 0; pass < 3; ++pass) {
@@ -142,55 +153,68 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const EvictParams p)
     for (int i = tid; i < nb; i += kPickThreads) sh_hist[i] = 0u;
     __syncthreads();
     const int top = shift + bits;
-    constexpr int kLoads = 8;
-    for (int t0 = c0; t0 < c1; t0 += kLoads * kPickThreads) {
-      float x[kLoads];
+    auto count = [&](int t, uint32_t key) {
+      if (t < c1 && (pass == 0 || (key >> top) == (prefix >> top))) atomicAdd(&sh_hist[(key >> shift) & (nb - 1)], 1u);
+    };
+    if (held) {
 #pragma unroll
-      for (int k = 0; k < kLoads; ++k) {
-        const int t = t0 + k * kPickThreads + tid;
-        x[k] = t < c1 ? __ldg(acc + t) : 0.f;
-      }
+      for (int k = 0; k < kPickKeys; ++k) count(c0 + k * kPickThreads + tid, keys[k]);
+    } else {
+      constexpr int kLoads = 8;
+      for (int t0 = c0; t0 < c1; t0 += kLoads * kPickThreads) {
+        float x[kLoads];
 #pragma unroll
-      for (int k = 0; k < kLoads; ++k) {
-        const uint32_t key = sum_key(x[k]);
-        const bool in = t0 + k * kPickThreads + tid < c1 && (pass == 0 || (key >> top) == (prefix >> top));
-        const uint32_t bin = (key >> shift) & (nb - 1);
-        // many sums are equal (zeros): one add per warp and bin
-        const uint32_t peers = __match_any_sync(0xffffffffu, in ? bin : 0xffffffffu);
-        if (in && (tid & 31) == __ffs(peers) - 1) atomicAdd(&sh_hist[bin], (uint32_t)__popc(peers));
+        for (int k = 0; k < kLoads; ++k) {
+          const int t = t0 + k * kPickThreads + tid;
+          x[k] = t < c1 ? __ldg(acc + t) : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k) count(t0 + k * kPickThreads + tid, sum_key(x[k]));
       }
     }
     cluster.sync();
-    const int per = nb / C;  // C is a power of two up to 16
+    const int per = nb / C;  // C is a power of two up to 8
     for (int i = tid; i < per; i += kPickThreads) {
-      uint32_t s = 0;
-      for (int r = 0; r < C; ++r) s += cluster.map_shared_rank(sh_hist, r)[rank * per + i];
-      cluster.map_shared_rank(sh_tot, 0)[rank * per + i] = s;
+      uint32_t sum = 0;
+#pragma unroll 4
+      for (int r = 0; r < C; ++r) sum += cluster.map_shared_rank(sh_hist, r)[rank * per + i];
+#pragma unroll 4
+      for (int r = 0; r < C; ++r) cluster.map_shared_rank(sh_tot, r)[rank * per + i] = sum;
     }
     cluster.sync();
-    if (rank == 0) {
-      int above;
-      const int bin = find_threshold_bin(sh_tot, nb, need, &above, sh_warp, sh_res);
-      if (tid < C) {
-        int *f = cluster.map_shared_rank(sh_found, tid);
-        f[0] = bin;
-        f[1] = above;
-      }
-    }
-    cluster.sync();
-    prefix |= (uint32_t)sh_found[0] << shift;
-    need -= sh_found[1];
+    int above;
+    const int bin = find_threshold_bin(sh_tot, nb, need, &above, sh_warp, sh_res);
+    prefix |= (uint32_t)bin << shift;
+    need -= above;
   }
-  // keys above `prefix` are all taken, `need` of the equal ones from the front
-  int gt = 0, eq = 0;
-  for (int t = c0 + tid; t < c1; t += kPickThreads) {
-    const uint32_t key = sum_key(__ldg(acc + t));
-    gt += key > prefix;
-    eq += key == prefix;
-  }
+  // Keys above `prefix` are all taken, `need` of the equal ones from the front. Both counts go in one word: at most
+  // 16,384 each of a share whose keys are held; a longer share counts its totals first and walks its positions again.
+  const int warp = tid >> 5, lane = tid & 31;
+  const uint32_t below = (1u << lane) - 1u;
   int tot_gt, tot_eq;
-  block_exclusive_scan(gt, sh_warp, &tot_gt);
-  block_exclusive_scan(eq, sh_warp, &tot_eq);
+  if (held) {
+#pragma unroll
+    for (int k = 0; k < kPickKeys; ++k) {
+      const bool in = c0 + k * kPickThreads + tid < c1;
+      const uint32_t mg = __ballot_sync(0xffffffffu, in && keys[k] > prefix), me = __ballot_sync(0xffffffffu, in && keys[k] == prefix);
+      if (lane == 0) sh_tot[k * 32 + warp] = (uint32_t)(__popc(mg) | (__popc(me) << 16));
+    }
+    __syncthreads();
+    int tot;
+    const int x = tid < kPickKeys * 32 ? (int)sh_tot[tid] : 0, before = block_exclusive_scan(x, sh_warp, &tot);
+    if (tid < kPickKeys * 32) sh_tot[tid] = (uint32_t)before;
+    tot_gt = tot & 0xffff;
+    tot_eq = tot >> 16;
+  } else {
+    int gt = 0, eq = 0;
+    for (int t = c0 + tid; t < c1; t += kPickThreads) {
+      const uint32_t key = sum_key(__ldg(acc + t));
+      gt += key > prefix;
+      eq += key == prefix;
+    }
+    block_exclusive_scan(gt, sh_warp, &tot_gt);
+    block_exclusive_scan(eq, sh_warp, &tot_eq);
+  }
   if (tid < C) cluster.map_shared_rank(sh_counts, tid)[rank] = make_int2(tot_gt, tot_eq);
   cluster.sync();
   int gt0 = 0, eq0 = 0;
@@ -198,10 +222,19 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const EvictParams p)
     gt0 += sh_counts[r].x;
     eq0 += sh_counts[r].y;
   }
+  if (held) {
+#pragma unroll
+    for (int k = 0; k < kPickKeys; ++k) {
+      const int t = c0 + k * kPickThreads + tid;
+      const bool is_gt = t < c1 && keys[k] > prefix, is_eq = t < c1 && keys[k] == prefix;
+      const uint32_t mg = __ballot_sync(0xffffffffu, is_gt), me = __ballot_sync(0xffffffffu, is_eq), before = sh_tot[k * 32 + warp];
+      const int g = gt0 + (int)(before & 0xffffu) + __popc(mg & below), e = eq0 + (int)(before >> 16) + __popc(me & below);
+      if (is_gt || (is_eq && e < need)) kept[g + min(e, need)] = t;
+    }
+    return;
+  }
   // in position order: a warp takes 128 positions as 4 rounds of 32 lanes
   constexpr int kTile = kPickThreads * 4;
-  const int warp = tid >> 5, lane = tid & 31;
-  const uint32_t below = (1u << lane) - 1u;
   for (int t0 = c0; t0 < c1; t0 += kTile) {
     uint32_t mg[4], me[4];
     int cg_ = 0, ce = 0;
@@ -214,7 +247,7 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const EvictParams p)
       cg_ += __popc(mg[r]);
       ce += __popc(me[r]);
     }
-    int tot;  // both counts in one scan: at most 2048 each
+    int tot;  // both counts in one scan: at most 4096 each
     const int scan = block_exclusive_scan(lane == 0 ? cg_ | (ce << 16) : 0, sh_warp, &tot);
     const int base = __shfl_sync(0xffffffffu, scan, 0);
     int g = gt0 + (base & 0xffff), e = eq0 + (base >> 16);
@@ -233,63 +266,149 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const EvictParams p)
 }
 
 // ------------------------------------------------------------------ move
-// Row kept[j] -> j of one unit, j ascending, in place: kept[j] >= j, so a CTA
-// that reads a run of rows before it writes them never overwrites a row that
-// is still to be read.  The rows cannot be dealt over CTAs without such an
-// order between them, but a row's columns can: a CTA owns `cols` bytes of one
-// unit's K or V rows (or its sums, or its scales) and walks all of them.
-constexpr int kMoveThreads = 512;
-constexpr int kMoveLoads = 4;
+// Row kept[j] -> j of one unit, j ascending, in place: kept[j] >= j, so rows that
+// are read in runs, each before it is written, are never overwritten unread.  A
+// cluster of CTAs moves one unit's K rows (V rows, sums, scales), each a part of
+// every run, whole rows each (32-byte columns of the same rows, a CTA each, took
+// 110 us for halving 4 x 65,536 tokens: DRAM reads 64 bytes at a time); a cluster
+// barrier stands between a run's reads and its writes.  Rows wait for their turn in
+// a ring in shared memory, so some 100 KB per SM are on the way without a register.
+// A row's two places are found once, by one thread, steps ahead of its copy.
+constexpr int kMoveThreads = 256;
+constexpr int kMoveRuns = 5;  // in the ring: one written, one awaited, three on the way
+constexpr int kMoveRows = 256;  // rows of a CTA's part of a run, at most
+
+struct MoveRing {
+  uint4 data[kMoveRuns][4 * kMoveThreads];
+  int32_t from[2][kMoveRows];        // of the run that is copied next, and the one after it
+  int32_t to[kMoveRuns][kMoveRows];  // -1: nothing moves
+};
 
 template <typename V>
-__device__ __forceinline__ void move_rows(uint8_t *base, int64_t row_bytes, int lanes, int col, const int32_t *kept, int K,
-                                          const EvictParams &p, int b, bool sums) {
-  const int per = kMoveThreads / lanes, tile = per * kMoveLoads;  // rows per round of loads, per tile
-  const int r0 = threadIdx.x / lanes;
-  for (int j0 = 0; j0 < K; j0 += tile) {
-    V x[kMoveLoads];
-    int64_t dst[kMoveLoads];
-#pragma unroll
-    for (int k = 0; k < kMoveLoads; ++k) {
-      const int j = j0 + k * per + r0;
-      dst[k] = -1;
-      if (j < K) {
-        const int t = __ldcg(kept + j);
-        if (t != j) {
-          const int64_t from = sums ? t : evict_slot(p.page_table, p.max_pages, p.page_size, p.num_slots, b, t);
-          const int64_t to = sums ? j : evict_slot(p.page_table, p.max_pages, p.page_size, p.num_slots, b, j);
-          if (from >= 0 && to >= 0) {
-            x[k] = __ldcg(reinterpret_cast<const V *>(base + from * row_bytes + col));
-            dst[k] = to;
-          }
-        }
-      }
-    }
-    __syncthreads();  // every row of the tile is read
-#pragma unroll
-    for (int k = 0; k < kMoveLoads; ++k)
-      if (dst[k] >= 0) *reinterpret_cast<V *>(base + dst[k] * row_bytes + col) = x[k];
-  }
+__device__ __forceinline__ void copy_async(uint32_t dst, const V *src) {
+  if constexpr (sizeof(V) == 16) cp_async_16(dst, src);
+  else cp_async_4(dst, src);
 }
 
-__global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictParams p) {
+// LOADS elements per thread and run; `lanes` elements per row
+template <typename V, int LOADS>
+__device__ __forceinline__ void move_rows(uint8_t *base, int64_t row_bytes, int lanes, int col, const int32_t *kept, int K,
+                                          const EvictParams &p, int b, bool sums, MoveRing &ring) {
+  cg::cluster_group cluster = cg::this_cluster();
+  const int per = kMoveThreads / lanes, rows = per * LOADS, run = rows * (int)cluster.num_blocks();
+  const int tid = threadIdx.x, r0 = tid / lanes, j_first = (int)cluster.block_rank() * rows;
+  const int32_t *pt = p.page_table && !sums ? p.page_table + (int64_t)b * p.max_pages : nullptr;
+  const uint32_t ps = (uint32_t)p.page_size;
+  // This thread's row of a run: its kept position, then the page numbers of both places, are fetched a step before they
+  // are looked at.
+  int t_far = -1, t = -1, pg_from = 0, pg_to = 0;
+  auto look = [&](int j0) {
+    const int j = j0 + j_first + tid;
+    t_far = tid < rows && j < K ? __ldcg(kept + j) : -1;
+  };
+  auto pages = [&](int j0) {
+    const int j = j0 + j_first + tid;
+    t = t_far == j ? -1 : t_far;
+    if (pt && t >= 0) {
+      pg_from = __ldg(pt + (uint32_t)t / ps);
+      pg_to = __ldg(pt + (uint32_t)j / ps);
+    }
+  };
+  auto places = [&](int j0, int at, int at2) {
+    if (tid >= rows) return;
+    int64_t from = t, to = j0 + j_first + tid;
+    if (!sums && t >= 0) {
+      from = pt ? (int64_t)pg_from * ps + (uint32_t)t % ps : (int64_t)b * ps + t;
+      to = pt ? (int64_t)pg_to * ps + (uint32_t)to % ps : (int64_t)b * ps + to;
+      if (from < 0 || from >= p.num_slots || to < 0 || to >= p.num_slots) to = -1;
+    }
+    ring.from[at2][tid] = (int32_t)from;
+    ring.to[at][tid] = t >= 0 ? (int32_t)to : -1;
+  };
+  V *data = reinterpret_cast<V *>(ring.data);
+  auto fetch = [&](int at, int at2) {
+#pragma unroll
+    for (int k = 0; k < LOADS; ++k) {
+      const int r = k * per + r0;
+      if (ring.to[at][r] >= 0)
+        copy_async(smem_u32(data + (at * LOADS + k) * kMoveThreads + tid),
+                   reinterpret_cast<const V *>(base + ring.from[at2][r] * row_bytes + col));
+    }
+    cp_async_commit();
+  };
+  auto write = [&](int at) {
+#pragma unroll
+    for (int k = 0; k < LOADS; ++k) {
+      const int to = ring.to[at][k * per + r0];
+      if (to >= 0) *reinterpret_cast<V *>(base + to * row_bytes + col) = data[(at * LOADS + k) * kMoveThreads + tid];
+    }
+  };
+  {  // places of runs 0 to 3, copies of runs 0 to 2: all of a kind at once
+    int kept_of[kMoveRuns + 1], from_of[kMoveRuns], to_of[kMoveRuns];
+#pragma unroll
+    for (int i = 0; i <= kMoveRuns; ++i) {
+      look(i * run);
+      kept_of[i] = t_far;
+    }
+#pragma unroll
+    for (int i = 0; i < kMoveRuns; ++i) {
+      t_far = kept_of[i];
+      pages(i * run);
+      from_of[i] = pg_from, to_of[i] = pg_to;
+    }
+#pragma unroll
+    for (int i = 0; i < kMoveRuns - 1; ++i) {
+      const int j = i * run + j_first + tid;
+      t = kept_of[i] == j ? -1 : kept_of[i];
+      pg_from = from_of[i], pg_to = to_of[i];
+      places(i * run, i, i & 1);
+      __syncthreads();
+      if (i < kMoveRuns - 2) fetch(i, i & 1);
+    }
+    const int j = (kMoveRuns - 1) * run + j_first + tid;
+    t = kept_of[kMoveRuns - 1] == j ? -1 : kept_of[kMoveRuns - 1];
+    pg_from = from_of[kMoveRuns - 1], pg_to = to_of[kMoveRuns - 1];
+    t_far = kept_of[kMoveRuns];
+  }
+  int at = 0, i = 0;  // the run that is awaited: its place, its number
+  for (int j0 = 0; j0 < K; j0 += run, ++i) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kMoveRuns - 3) : "memory");
+    if (j0 > 0) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    // This CTA's part of the run is read: it is in shared memory, so the barrier has nothing to order (a release would
+    // wait for the last run's writes, 1.5 us a step).
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    const int before = at == 0 ? kMoveRuns - 1 : at - 1, next = at < 2 ? at + 3 : at - 2;  // runs i - 1 and i + 3
+    if (j0 > 0) write(before);
+    __syncthreads();  // run i + 3's places are there, and run i - 1 has left its own: run i + 4's
+    fetch(next, (i + 3) & 1);
+    places(j0 + (kMoveRuns - 1) * run, before, i & 1);
+    pages(j0 + kMoveRuns * run);
+    look(j0 + (kMoveRuns + 1) * run);
+    at = at == kMoveRuns - 1 ? 0 : at + 1;
+  }
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  write(at == 0 ? kMoveRuns - 1 : at - 1);
+  cp_async_wait_all();
+}
+__global__ void __launch_bounds__(kMoveThreads, 2) move_kernel(const EvictParams p) {
+  extern __shared__ __align__(16) uint8_t move_smem[];
+  MoveRing &move_ring = *reinterpret_cast<MoveRing *>(move_smem);
   griddep_wait();
   griddep_launch_dependents();
-  const int u = blockIdx.x, b = u / p.Hkv, kvh = u % p.Hkv;
+  const int u = blockIdx.x / (int)cg::this_cluster().num_blocks(), b = u / p.Hkv, kvh = u % p.Hkv, job = blockIdx.y;
   const int T = clamp_len(__ldg(p.seq_lens + b), (int)p.t_cap);
-  if (T <= p.budget) return;
+  if (T <= p.budget) return;  // the same for the cluster
   const int32_t *kept = p.kept + (int64_t)u * p.budget;
-  const int chunks = p.head_bytes / p.cols, job = blockIdx.y;
-  if (job < 2 * chunks) {
-    uint8_t *x = static_cast<uint8_t *>(job < chunks ? p.k : p.v);
-    const int lanes = p.cols / 16;
-    move_rows<uint4>(x, (int64_t)p.Hkv * p.head_bytes, lanes,
-                     kvh * p.head_bytes + (job % chunks) * p.cols + (threadIdx.x % lanes) * 16, kept, p.budget, p, b, false);
-  } else if (job == 2 * chunks) {
-    move_rows<float>(reinterpret_cast<uint8_t *>(p.acc + (int64_t)u * p.acc_stride), 4, 1, 0, kept, p.budget, p, b, true);
+  const int64_t row_bytes = (int64_t)p.Hkv * p.head_bytes;
+  if (job < 2) {
+    const int lanes = p.head_bytes / 16;
+    move_rows<uint4, 4>(static_cast<uint8_t *>(job == 0 ? p.k : p.v), row_bytes, lanes, kvh * p.head_bytes + (threadIdx.x % lanes) * 16,
+                     kept, p.budget, p, b, false, move_ring);
+  } else if (job == 2) {
+    move_rows<float, 1>(reinterpret_cast<uint8_t *>(p.acc + (int64_t)u * p.acc_stride), 4, 1, 0, kept, p.budget, p, b, true, move_ring);
   } else {
-    move_rows<float>(reinterpret_cast<uint8_t *>(job == 2 * chunks + 1 ? p.k_scale : p.v_scale), (int64_t)p.Hkv * 4, 1,
-                     kvh * 4, kept, p.budget, p, b, false);
+    move_rows<float, 1>(reinterpret_cast<uint8_t *>(job == 3 ? p.k_scale : p.v_scale), (int64_t)p.Hkv * 4, 1, kvh * 4, kept, p.budget,
+                     p, b, false, move_ring);
   }
 }
 
@@ -304,18 +423,18 @@ cudaError_t launch_accept(const AcceptParams &p, bool scales, cudaStream_t s) {
 cudaError_t launch_evict(const EvictParams &p0, bool scales, int sms, cudaStream_t s) {
   EvictParams p = p0;
   const int units = p.B * p.Hkv;
-  int C = 1;  // shares of at least 2,048 positions, and no more CTAs than fit beside each other
-  while (C < 16 && p.t_cap > (int64_t)C * 4096 && (int64_t)units * C * 2 <= 4 * sms) C *= 2;
+  int C = 1;  // shares of at least 2,048 positions, and no more CTAs than SMs
+  while (C < 8 && p.t_cap > (int64_t)C * 4096 && (int64_t)units * C * 2 <= sms) C *= 2;
   cudaError_t e;
-  if (C > 8 && (e = allow_wide_clusters_once(reinterpret_cast<const void *>(pick_kernel))) != cudaSuccess) return e;
   e = launch_ex(pick_kernel, dim3((unsigned)(units * C)), dim3(kPickThreads), 0, s, C, p);
   if (e != cudaSuccess) return e;
-  // columns per CTA: whole rows when the units alone fill the GPU, down to a
-  // 32-byte sector when there are few
-  p.cols = p.head_bytes;
-  while (p.cols > 32 && (int64_t)units * 2 * (p.head_bytes / p.cols) < 2 * sms) p.cols /= 2;
-  const int jobs = 2 * (p.head_bytes / p.cols) + 1 + (scales ? 2 : 0);
-  return launch_ex(move_kernel, dim3((unsigned)units, jobs), dim3(kMoveThreads), 0, s, 0, p);
+  // CTAs per unit and job: no more than fit beside each other (two per SM), and a
+  // run of theirs (at least 32 rows each) no longer than the budget
+  C = 1;
+  const int jobs = scales ? 5 : 3;
+  while (C < 8 && (int64_t)units * 2 * C * 2 <= 2 * sms && p.budget > C * 64) C *= 2;
+  if ((e = set_smem_once(reinterpret_cast<const void *>(move_kernel), (int)sizeof(MoveRing))) != cudaSuccess) return e;
+  return launch_ex(move_kernel, dim3((unsigned)(units * C), jobs), dim3(kMoveThreads), (int)sizeof(MoveRing), s, C, p);
 }
 
 }  // namespace hs2

@@ -236,7 +236,6 @@ struct EvictParams {
   int32_t *lens_out;
   int32_t B, Hkv, budget, window;
   int32_t head_bytes;                // one head's row of K or V
-  int32_t cols;                      // bytes of it per CTA (set by launch_evict)
   int32_t page_size, max_pages;
   int64_t t_cap, num_slots;
 };
@@ -276,9 +275,7 @@ struct TreeParams {
   int32_t *prefix;                   // [B + 1] tiles before sequence b,
   float *records;                    // [groups][kTreeSlots][blocks][streams] of rows * (D + 2)
 };
-int tree_f32_rows();
-int tree_f32_tile();
-int tree_f32_ctas_per_sm(int D);
+int tree_f32_ctas_per_sm(int D, int rows, int keys);
 cudaError_t launch_tree_f32(const TreeParams &p, cudaStream_t s);
 int tree_tc_rows();
 int tree_tc_tile();

@@ -8,7 +8,8 @@
 // fp32 caches keep fp32 products on the CUDA cores (tensor cores would round
 // the operands): a CTA of 16 x 16 threads takes 64 rows x 64 positions, each
 // thread a 4 x 4 block of the logits and 4 rows x D / 16 columns of the output
-// in registers; Q, K, V and the weights are in shared memory, K's and Q's rows
+// in registers (half the rows where a unit has at most 32, and half the positions
+// where the tiles would not fill the GPU); Q, K, V and the weights are in shared memory, K's and Q's rows
 // padded by 16 bytes so that 16-byte reads of 8 rows meet 32 banks.
 #include <type_traits>
 
@@ -20,9 +21,9 @@ namespace hs2 {
 
 namespace {
 
-constexpr int kRows = 64, kKeys = 64, kThreads = 256;
+constexpr int kThreads = 256;
 
-template <int D>
+template <int D, int kRows, int kKeys>
 struct TreeF32Smem {
   static constexpr int QS = D + 4, PS = kKeys + 4;
   static constexpr size_t kQ = 0, kK = kQ + (size_t)kRows * QS * 4, kV = kK + (size_t)kKeys * QS * 4,
@@ -31,9 +32,10 @@ struct TreeF32Smem {
   static size_t bytes(int B) { return kPrefix + (size_t)(B + 1) * 4; }
 };
 
-template <int D>
+template <int D, int kRows, int kKeys>
 __global__ void __launch_bounds__(kThreads) tree_f32_kernel(const TreeParams p) {
-  using S = TreeF32Smem<D>;
+  using S = TreeF32Smem<D, kRows, kKeys>;
+  constexpr int R = kRows / 16, K = kKeys / 16;  // rows and positions of a thread
   extern __shared__ __align__(16) uint8_t smem[];
   float *sq = reinterpret_cast<float *>(smem + S::kQ), *sk = reinterpret_cast<float *>(smem + S::kK);
   float *sv = reinterpret_cast<float *>(smem + S::kV), *sp = reinterpret_cast<float *>(smem + S::kP);
@@ -50,7 +52,7 @@ __global__ void __launch_bounds__(kThreads) tree_f32_kernel(const TreeParams p) 
     for (int i = tid; i <= p.B; i += kThreads) p.prefix[i] = prefix[i];
   const int64_t total = (int64_t)p.Hkv * prefix[p.B];
   if (total == 0) return;
-  const TreeShare share{total, p.groups};
+  const TreeShare share(total, p.groups);
   const int64_t g1 = share.start(group + 1);
   for (int64_t g = share.start(group); g < g1;) {
     // one segment: tiles [i0, i1) of unit (b, kvh)
@@ -74,9 +76,9 @@ __global__ void __launch_bounds__(kThreads) tree_f32_kernel(const TreeParams p) 
     }
     for (int row = tid; row < kRows; row += kThreads)
       bits[row] = row < nrows ? tree_bits(p, b, (row0 + row) / p.G, n) : 0ull;
-    float o[4][D / 16], m[4], l[4];
+    float o[R][D / 16], m[R], l[R];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < R; ++i) {
       m[i] = -INFINITY;
       l[i] = 0.f;
 #pragma unroll
@@ -98,31 +100,31 @@ __global__ void __launch_bounds__(kThreads) tree_f32_kernel(const TreeParams p) 
         *reinterpret_cast<float4 *>(sv + row * D + d) = v4;
       }
       __syncthreads();
-      float s[4][4];
+      float s[R][K];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < R; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+        for (int j = 0; j < K; ++j) s[i][j] = 0.f;
 #pragma unroll 4
       for (int d = 0; d < D; d += 4) {
-        float4 a[4], k4[4];
+        float4 a[R], k4[K];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4 *>(sq + (ty * 4 + i) * S::QS + d);
+        for (int i = 0; i < R; ++i) a[i] = *reinterpret_cast<const float4 *>(sq + (ty * R + i) * S::QS + d);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) k4[j] = *reinterpret_cast<const float4 *>(sk + (tx + 16 * j) * S::QS + d);
+        for (int j = 0; j < K; ++j) k4[j] = *reinterpret_cast<const float4 *>(sk + (tx + 16 * j) * S::QS + d);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < R; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
+          for (int j = 0; j < K; ++j)
             s[i][j] = fmaf(a[i].x, k4[j].x, fmaf(a[i].y, k4[j].y, fmaf(a[i].z, k4[j].z, fmaf(a[i].w, k4[j].w, s[i][j]))));
       }
       const bool plain = p0 + kKeys <= first;  // a tile of the context alone: all of it is seen
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint64_t mk = bits[ty * 4 + i];
+      for (int i = 0; i < R; ++i) {
+        const uint64_t mk = bits[ty * R + i];
         float mx = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < K; ++j) {
           s[i][j] *= p.c2;
           if (!plain) {
             const int t = p0 + tx + 16 * j;
@@ -137,10 +139,10 @@ __global__ void __launch_bounds__(kThreads) tree_f32_kernel(const TreeParams p) 
         m[i] = m_new;
         float sum = 0.f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < K; ++j) {
           const float w = exp2f(s[i][j] - at);
           sum += w;
-          sp[(ty * 4 + i) * S::PS + tx + 16 * j] = w;
+          sp[(ty * R + i) * S::PS + tx + 16 * j] = w;
         }
 #pragma unroll
         for (int w = 8; w; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
@@ -153,10 +155,10 @@ __global__ void __launch_bounds__(kThreads) tree_f32_kernel(const TreeParams p) 
       auto add_values = [&](auto hide) {
 #pragma unroll 2
         for (int t = 0; t < kKeys; t += 4) {
-          float w[4][4];
+          float w[R][4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float4 x = *reinterpret_cast<const float4 *>(sp + (ty * 4 + i) * S::PS + t);
+          for (int i = 0; i < R; ++i) {
+            const float4 x = *reinterpret_cast<const float4 *>(sp + (ty * R + i) * S::PS + t);
             w[i][0] = x.x, w[i][1] = x.y, w[i][2] = x.z, w[i][3] = x.w;
           }
 #pragma unroll
@@ -166,7 +168,7 @@ __global__ void __launch_bounds__(kThreads) tree_f32_kernel(const TreeParams p) 
               const float4 v4 = *reinterpret_cast<const float4 *>(sv + (t + tt) * D + k * 64 + tx * 4);
               const float v[4] = {v4.x, v4.y, v4.z, v4.w};
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
+              for (int i = 0; i < R; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                   const float x = decltype(hide)::value && w[i][tt] == 0.f ? 0.f : v[e];
@@ -182,8 +184,8 @@ __global__ void __launch_bounds__(kThreads) tree_f32_kernel(const TreeParams p) 
     const bool begins_share = g - (i1 - i0) == share.start(group);
     float *rec = whole ? nullptr : tree_record(p, group, begins_share ? 0 : 1, block, 0);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = ty * 4 + i;
+    for (int i = 0; i < R; ++i) {
+      const int row = ty * R + i;
       if (row >= nrows) continue;
       if (whole) {
         const float inv = l[i] > 0.f || l[i] != l[i] ? 1.f / l[i] : 0.f;  // nothing seen: zeros
@@ -227,7 +229,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) tree_combine_kernel(const 
   const int64_t total = (int64_t)p.Hkv * p.prefix[p.B];
   const int nb = p.prefix[b + 1] - p.prefix[b];
   if (nb == 0) return;
-  const TreeShare share{total, p.groups};
+  const TreeShare share(total, p.groups);
   const int64_t U0 = (int64_t)p.Hkv * p.prefix[b] + (int64_t)kvh * nb;
   const int64_t c0 = share.owner(U0), c1 = share.owner(U0 + nb - 1);
   // 32 rows lie in one block, and in one stream's rows
@@ -288,9 +290,10 @@ __global__ void __launch_bounds__(32 * kCombineWarps) tree_combine_kernel(const 
 
 }  // namespace
 
-int tree_f32_rows() { return kRows; }
-int tree_f32_tile() { return kKeys; }
-int tree_f32_ctas_per_sm(int D) { return D == 64 ? 3 : 1; }
+int tree_f32_ctas_per_sm(int D, int rows, int keys) {
+  if (D == 64) return rows == 32 && keys == 32 ? 3 : 2;
+  return rows == 32 ? 2 : 1;
+}
 
 cudaError_t launch_tree_f32(const TreeParams &p, cudaStream_t s) {
   auto run = [&](auto kern, size_t bytes) {
@@ -298,7 +301,15 @@ cudaError_t launch_tree_f32(const TreeParams &p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     return launch_ex(kern, dim3((unsigned)(p.groups * p.blocks)), dim3(kThreads), bytes, s, 0, p);
   };
-  return p.D == 64 ? run(tree_f32_kernel<64>, TreeF32Smem<64>::bytes(p.B)) : run(tree_f32_kernel<128>, TreeF32Smem<128>::bytes(p.B));
+  auto shape = [&](auto rows, auto keys) {
+    constexpr int R = decltype(rows)::value, K = decltype(keys)::value;
+    return p.D == 64 ? run(tree_f32_kernel<64, R, K>, TreeF32Smem<64, R, K>::bytes(p.B))
+                     : run(tree_f32_kernel<128, R, K>, TreeF32Smem<128, R, K>::bytes(p.B));
+  };
+  using S32 = std::integral_constant<int, 32>;
+  using S64 = std::integral_constant<int, 64>;
+  if (p.rows == 32) return p.tile == 32 ? shape(S32{}, S32{}) : shape(S32{}, S64{});
+  return shape(S64{}, S64{});
 }
 
 cudaError_t launch_tree_combine(const TreeParams &p, bool f32, cudaStream_t s) {

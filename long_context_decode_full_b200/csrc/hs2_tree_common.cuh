@@ -24,10 +24,13 @@ namespace hs2 {
 
 namespace {
 
+// The tiles of every share; with fewer tiles than shares the last shares are empty.
 struct TreeShare {
   int64_t total;  // Hkv * sum_b tiles
   int32_t groups;
-  __device__ __forceinline__ int64_t start(int64_t c) const { return c * total / groups; }
+  __device__ __forceinline__ TreeShare(int64_t tiles, int32_t shares)
+      : total(tiles), groups((int32_t)min((int64_t)shares, tiles > 0 ? tiles : 1)) {}
+  __device__ __forceinline__ int64_t start(int64_t c) const { return min(c, (int64_t)groups) * total / groups; }
   __device__ __forceinline__ int64_t owner(int64_t x) const { return ((x + 1) * groups - 1) / total; }
 };
 

@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     total *= p.Hkv;
     if (total > 0) {
-      const TreeShare share{total, p.groups};
+      const TreeShare share(total, p.groups);
       const int64_t g0 = share.start(group);
       int64_t carry = 0;
       for (int b0 = 0; b0 < p.B; b0 += 32) {
