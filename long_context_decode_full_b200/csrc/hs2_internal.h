@@ -207,7 +207,6 @@ struct RopeParams {
   int32_t B, N, Hq, Hkv, D;
   int32_t page_size, max_pages;
   int64_t t_cap, num_slots;
-  int32_t tokens_per_cta;            // set by launch_rope
 };
 cudaError_t launch_rope(const RopeParams &p, int sms, cudaStream_t s);
 

@@ -421,12 +421,12 @@ def _arg(name, t, dtype, shape):
 
 def _paged(k, v, k_scale, v_scale, page_table, page_size, B):
     """Checked cache descriptors, the page table's pointer and max_pages."""
-    shape, pages, max_pages = k.shape, None, 1
-    for name, x in (("k", k), ("v", v)):
-        if x.dtype not in _DTYPE:
-            raise HS2Error(ERR_INVALID_ARG, f"{name}: dtype {x.dtype} is no cache type")
-        if x.dim() != 3 or not x.is_contiguous():
-            raise HS2Error(ERR_INVALID_ARG, f"{name}: expected a contiguous [num_slots, Hkv, d] cache")
+    kd, vd, shape, v_shape = _DTYPE.get(k.dtype), _DTYPE.get(v.dtype), k.shape, v.shape
+    if kd is None or vd is None:
+        raise HS2Error(ERR_INVALID_ARG, f"k, v: dtype {k.dtype}, {v.dtype} is no cache type")
+    if len(shape) != 3 or len(v_shape) != 3 or not k.is_contiguous() or not v.is_contiguous():
+        raise HS2Error(ERR_INVALID_ARG, "k, v: expected contiguous [num_slots, Hkv, d] caches")
+    pages, max_pages = None, 1
     if page_table is not None:
         if page_size is None:
             raise HS2Error(ERR_INVALID_ARG, "page_size is required with a page table")
@@ -434,9 +434,10 @@ def _paged(k, v, k_scale, v_scale, page_table, page_size, B):
         pages = _arg("page_table", page_table, torch.int32, (B, max_pages))
     elif page_size is None:
         page_size = shape[0] // max(B, 1)
-    ks, vs = _arg("k_scale", k_scale, torch.float32, shape[:2]), _arg("v_scale", v_scale, torch.float32, v.shape[:2])
-    return (Cache(k.data_ptr(), ks, _DTYPE[k.dtype], shape[1], shape[2], page_size, shape[0]),
-            Cache(v.data_ptr(), vs, _DTYPE[v.dtype], v.shape[1], v.shape[2], page_size, v.shape[0]), pages, max_pages)
+    ks = None if k_scale is None else _arg("k_scale", k_scale, torch.float32, shape[:2])
+    vs = None if v_scale is None else _arg("v_scale", v_scale, torch.float32, v_shape[:2])
+    return (Cache(k.data_ptr(), ks, kd, shape[1], shape[2], page_size, shape[0]),
+            Cache(v.data_ptr(), vs, vd, v_shape[1], v_shape[2], page_size, v_shape[0]), pages, max_pages)
 
 
 def _tokens(name, x, dtype) -> Tokens:

@@ -432,6 +432,30 @@ def test_rope_append(case, N):
         assert torch.equal(R.bits(q2[b, :n]), R.bits(q_out[b, :n])) and torch.equal(R.bits(q2[b, n:]), R.bits(qkv[b, n:, :hq]))
 
 
+def test_rope_append_e4m3_rows_of_any_size():
+    """Rows of subnormal, tiny and huge elements, and rows with one large element: scale and codes as for any other."""
+    c = R.PagedCache("e4m3", [40], 2, 128, 16, seed=1)
+    x = torch.randn(1, 8, 2, 128, device="cuda", generator=gen(7))
+    x *= torch.tensor([1e-39, 1e-37, 1e-30, 1.0, 1e30, 1e37, 1.0, 1.0], device="cuda").view(1, 8, 1, 1)
+    x[0, 6, :, 3] = 1e20
+    x[0, 7, :, 1:] = 0
+    x = x.bfloat16()
+    pos = torch.zeros(1, 8, dtype=torch.int32, device="cuda")
+    hs2.rope_append(None, x, x, pos, hs2.rope_table(128), c.k, c.v, c.lens, **c.kw())
+    for i in range(8):
+        slot, want = int(c.slots(0, 32 + i)), x[0, i].double()
+        for cache, sc in ((c.k, c.k_scale), (c.v, c.v_scale)):
+            s = sc[slot].double()
+            top = want.abs().amax(-1)
+            # one rounding of max / 448, which may be subnormal
+            assert bool(((s - top / 448).abs() <= top / 448 * 2.0 ** -23 + 2.0 ** -149).all())
+            err = (cache[slot].double() * s.unsqueeze(-1) - want).abs()
+            # half a step of the code (a subnormal one: 2^-10 of the scale), the quotient's error of two roundings, and the
+            # half unit by which a subnormal scale is off, taken 448 times
+            tol = 2.0 ** -4 * want.abs() * (1 + 2.0 ** -6) + s.unsqueeze(-1) * 2.0 ** -10 + 448 * 2.0 ** -149
+            assert bool((err <= tol).all()), (i, float((err - tol).max()))
+
+
 def test_rope_append_page_outside_the_cache():
     c = R.PagedCache("bf16", [40, 40], 2, 128, 16, seed=1)
     c.table[1, 2] = 2 ** 31 - 1  # the page of positions 32 to 47
