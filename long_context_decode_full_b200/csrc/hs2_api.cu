@@ -232,6 +232,8 @@ int check_caches(const hs2_cache *k, const hs2_cache *v) {
   if (!aligned16(k->data) || !aligned16(v->data)) return fail(HS2_ERR_INVALID_ARG, "cache data not 16-byte aligned");
   if (k->dtype == HS2_E4M3) {
     if (!k->scale || !v->scale) return fail(HS2_ERR_INVALID_ARG, "E4M3 caches need k and v scales");
+    if ((reinterpret_cast<uintptr_t>(k->scale) | reinterpret_cast<uintptr_t>(v->scale)) & 3)
+      return fail(HS2_ERR_INVALID_ARG, "scales are misaligned");
   } else if (k->scale || v->scale) {
     return fail(HS2_ERR_INVALID_ARG, "scales are only used with HS2_E4M3 caches");
   }

@@ -63,12 +63,13 @@ struct TreeTc {
   static constexpr int kPanels = kTile / kPanel;
   static constexpr int kStagesK = FP8 ? 3 : (D == 128 ? 5 : 8), kStagesV = FP8 ? 2 : 0;  // bf16: V has no ring of its own
   static constexpr int kStages = kStagesK + kStagesV;
-  static constexpr int kSlots = 2;  // tiles in the values warpgroup's hands
+  static constexpr int kSlots = 2;   // tiles in the values warpgroup's hands
+  static constexpr int kScales = 8;  // tiles whose scales are there or on the way: their fetch takes longer than a tile's logits
   static constexpr size_t oStage = 2 * kQ, oVals = oStage + (size_t)kStages * kTile, oScale = oVals + kSlots * kVals,
-                          oBar = oScale + (FP8 ? kSlots * 2 * kKeys * 4 : 0);
+                          oBar = oScale + (FP8 ? kScales * 2 * kKeys * 4 : 0);
   // p_full and o_full: a stream's halves of a tile
-  // full[S], empty[S], q_full[2], s_full[2], p_full[2][2], o_full[2][2], and per slot v_ready, v_free, scale_full, v_landed; done
-  static constexpr int kBars = 2 * kStages + 12 + 4 * kSlots + 1;
+  // full[S], empty[S], q_full[2], s_full[2], p_full[2][2], o_full[2][2], and per slot v_ready, v_free, v_landed; scale_full[8], scale_free[8]; done
+  static constexpr int kBars = 2 * kStages + 12 + 3 * kSlots + 2 * kScales + 1;
   static constexpr size_t oBad = oBar + (size_t)((kBars * 8 + 15) / 16 * 16), oInfo = oBad + 8 * kSlots, kBytes = oInfo + 64 + 1024;
   static_assert(kBytes <= 232448, "shared memory of a CTA");
 };
@@ -200,6 +201,11 @@ __device__ __forceinline__ void cp_async_4_or_zero(uint32_t dst, const void *src
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 // shared loads that stay where they are written
+__device__ __forceinline__ float4 lds_float4(const float *p) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(smem_u32(p)));
+  return v;
+}
 __device__ __forceinline__ float2 lds_float2(const float *p) {
   float2 v;
   asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(smem_u32(p)));
@@ -334,10 +340,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::oBar);
-  constexpr int kSlots = C::kSlots, SK = C::kStagesK, SV = C::kStagesV;
+  constexpr int kSlots = C::kSlots, kScales = C::kScales, SK = C::kStagesK, SV = C::kStagesV;
   uint64_t *full = bars, *empty = bars + S, *q_full = bars + 2 * S, *s_full = q_full + 2, *p_full = q_full + 4,
-           *o_full = q_full + 8, *v_ready = q_full + 12, *v_free = v_ready + kSlots, *scale_full = v_free + kSlots,
-           *v_landed = scale_full + kSlots, *done = v_landed + kSlots;
+           *o_full = q_full + 8, *v_ready = q_full + 12, *v_free = v_ready + kSlots, *v_landed = v_free + kSlots,
+           *scale_full = v_landed + kSlots, *scale_free = scale_full + kScales, *done = scale_free + kScales;
   volatile uint64_t *bad_rows = reinterpret_cast<volatile uint64_t *>(smem + C::oBad);
   TreeInfo *info = reinterpret_cast<TreeInfo *>(smem + C::oInfo);
   volatile int32_t *abort = &info->abort;
@@ -351,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(p_full + 2 * s, 4);
       mbar_init(p_full + 2 * s + 1, 4);
     }
-    for (int s = 0; s < kSlots; ++s) mbar_init(scale_full + s, 64);
+    for (int s = 0; s < kScales; ++s) mbar_init(scale_full + s, 64);
     fence_mbar_init();
     info->abort = 0;
     info->g0 = info->g1 = 0;
@@ -505,9 +511,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t slot_id = hc % kSlots, slot_parity = hc / kSlots & 1u;
         wait_or_abort(s_full + s, ns & 1u, abort, p.err, kErrFullWait);
         tc::fence_after();
-        if (FP8) wait_or_abort(scale_full + slot_id, slot_parity, abort, p.err, kErrFullWait);
+        if (FP8) wait_or_abort(scale_full + hc % kScales, hc / kScales & 1u, abort, p.err, kErrFullWait);
         if (special) wait_or_abort(v_ready + slot_id, slot_parity, abort, p.err, kErrFullWait);
-        const float *ks = reinterpret_cast<const float *>(smem + C::oScale) + slot_id * 2 * kKeys, *vs = ks + kKeys;
+        const float *ks = reinterpret_cast<const float *>(smem + C::oScale) + hc % kScales * 2 * kKeys, *vs = ks + kKeys;
         const uint64_t bad = special ? bad_rows[slot_id] : 0ull;
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
@@ -536,14 +542,19 @@ __global__ void __launch_bounds__(kThreads, 1)
               float2 sums[2] = {{0.f, 0.f}, {0.f, 0.f}};
               tmem_ld64(tx, x);
 #pragma unroll
-              for (int e = 0; e < 64; e += 2) {
-                float2 a = make_float2(x[e], x[e + 1]), kc = cc;
-                if constexpr (FP8) kc = mul2(cc, lds_float2(ks + 64 * h + e));
-                a = fma2(a, kc, sh);
-                a.x = ex2_approx(a.x), a.y = ex2_approx(a.y);
-                sums[(e >> 1) & 1] = add2(sums[(e >> 1) & 1], a);
-                if constexpr (FP8) a = mul2(a, lds_float2(vs + 64 * h + e));
+              for (int e = 0; e < 64; e += 4) {
+                float2 k0 = cc, k1 = cc, v0, v1;
+                if constexpr (FP8) {
+                  const float4 f = lds_float4(ks + 64 * h + e), g = lds_float4(vs + 64 * h + e);
+                  k0 = mul2(cc, make_float2(f.x, f.y)), k1 = mul2(cc, make_float2(f.z, f.w));
+                  v0 = make_float2(g.x, g.y), v1 = make_float2(g.z, g.w);
+                }
+                float2 a = fma2(make_float2(x[e], x[e + 1]), k0, sh), b = fma2(make_float2(x[e + 2], x[e + 3]), k1, sh);
+                a.x = ex2_approx(a.x), a.y = ex2_approx(a.y), b.x = ex2_approx(b.x), b.y = ex2_approx(b.y);
+                sums[0] = add2(sums[0], a), sums[1] = add2(sums[1], b);
+                if constexpr (FP8) a = mul2(a, v0), b = mul2(b, v1);
                 w[e >> 1] = pack_bf16(a.x, a.y);
+                w[(e >> 1) + 1] = pack_bf16(b.x, b.y);
               }
               const float2 both = add2(sums[0], sums[1]);
               sum = both.x + both.y;
@@ -845,7 +856,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t base = smem_u32(smem), bar = smem_u32(bars), tm = uniform(tmem);
       const uint32_t q0 = desc_lo(base, 16), k0 = desc_lo(base + (uint32_t)C::oStage, 16),
                      v0 = desc_lo(base + (uint32_t)(FP8 ? C::oVals : C::oStage), kKeys * 128);
-      const uint32_t b_empty = bar + 8 * S, b_s = bar + 8 * (2 * S + 2), b_o = bar + 8 * (2 * S + 8), b_free = bar + 8 * (2 * S + 12 + kSlots);
+      const uint32_t b_empty = bar + 8 * S, b_s = bar + 8 * (2 * S + 2), b_o = bar + 8 * (2 * S + 8), b_free = bar + 8 * (2 * S + 12 + kSlots),
+                     b_scale = bar + 8 * (2 * S + 12 + 3 * kSlots + kScales);
       uint32_t hc = 0;
       TreeRing ring{0, 0};
       uint32_t np = 0, nq = 0;  // parities of each stream's weights and queries, a bit each
@@ -886,7 +898,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < nt; ++i) {
           const bool handled = FP8 || seg.i0 + i >= seg.special0;
-          const uint32_t slot = uniform(hc % kSlots), stage = FP8 ? 0 : wait_full();
+          const uint32_t slot = uniform(hc % kSlots), scale_slot = uniform(hc % kScales), stage = FP8 ? 0 : wait_full();
           if (handled) {
             if (!FP8 && lane == 0) mbar_arrive(v_landed + slot);
             wait_or_abort(v_ready + slot, hc / kSlots & 1u, abort, p.err, kErrFullWait);
@@ -907,6 +919,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (last && !FP8) commit_one(b_empty + 8 * stage, one);
             if (last && handled) commit_one(b_free + 8 * slot, one);
+            if (last && FP8) commit_one(b_scale + 8 * scale_slot, one);
             if (i + ahead < nt) {
               if (first) next = wait_full();
               logits(s, next);
@@ -936,8 +949,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int k = 0; k < 2; ++k) next[k][0] = pages[k].next(p, seg.T), next[k][1] = pages[k].next(p, seg.T);
         for (int i = 0; i < nt; ++i, ++hc) {
-          const uint32_t slot_id = hc % kSlots;
-          wait_or_abort(v_free + slot_id, (hc / kSlots & 1u) ^ 1u, abort, p.err, kErrEmptyWait);
+          const uint32_t slot_id = hc % kScales;
+          wait_or_abort(scale_free + slot_id, (hc / kScales & 1u) ^ 1u, abort, p.err, kErrEmptyWait);
 #pragma unroll
           for (int k = 0; k < 2; ++k) {  // rows that are not there get 0
             const int64_t at = TreePages::slot(p, seg, next[k][0]);

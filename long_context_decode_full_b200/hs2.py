@@ -529,7 +529,9 @@ def alloc_tree_workspace(q, k) -> torch.Tensor:
         n = tree_workspace_bytes(B, N, k.shape[1], Hq // k.shape[1], d, _DTYPE[k.dtype])
     if n == 0:
         raise HS2Error(ERR_INVALID_ARG, "invalid workspace shape")
-    return torch.zeros(n, dtype=torch.uint8, device=k.device)
+    workspace = torch.empty(n, dtype=torch.uint8, device=k.device)
+    workspace[:256].zero_()  # the sticky error flag
+    return workspace
 
 
 def tree_attn(q, k, v, seq_lens, page_table=None, page_size=None, tree_mask=None, num_draft=None, k_scale=None,

@@ -56,6 +56,7 @@ def rope(q=tokens(), k=tokens(h=2), v=tokens(h=2), pos=FAKE, table=FAKE, rot=128
     (dict(pages=1 << 20), hs2.ERR_UNSUPPORTED),
     (dict(kc=cache(dtype=2), vc=cache(dtype=2)), hs2.ERR_INVALID_ARG),
     (dict(vc=cache(page=32)), hs2.ERR_INVALID_ARG),
+    (dict(kc=cache(dtype=2, scale=FAKE), vc=cache(dtype=2, scale=FAKE + 2)), hs2.ERR_INVALID_ARG),
 ])
 def test_rope_append_refuses(libhs2, kw, code):
     assert rope(**kw) == code

@@ -354,6 +354,27 @@ def test_cache_evict(dtype, hkv, d, page, budget, window):
         assert x is None or torch.equal(R.bits(x[untouched]), R.bits(y[untouched]))
 
 
+@pytest.mark.parametrize("T,budget,window,hkv", [(300000, 150001, 128, 1), (131072, 70000, 0, 1), (140000, 1000, 5, 2)])
+def test_cache_evict_long(T, budget, window, hkv):
+    """Shares of more positions than a CTA's registers hold, and many runs of rows; a short sequence beside."""
+    c = R.PagedCache("e4m3", [T, budget // 2], hkv, 128, 64, seed=13, poison=False)
+    acc = torch.exp(3 * torch.randn(2, hkv, c.cap, device="cuda", generator=gen(14)))
+    acc[acc < 1.0] = 0.0  # more zeros than are dropped: the last ones taken are among equals
+    acc0, before = acc.clone(), c.snapshot()
+    lens_out, kept = hs2.cache_evict(c.k, c.v, c.lens, acc, budget, window, **c.kw())
+    assert lens_out.tolist() == [budget, budget // 2]
+    for h in range(hkv):
+        keep = torch.tensor(R.kept_positions(acc0[0, h, :T].tolist(), T, budget, window), device="cuda")
+        assert torch.equal(kept[0, h].long(), keep)
+        src, dst = c.slots(0, keep), c.slots(0, torch.arange(budget))
+        for x, y in zip((c.k, c.v, c.k_scale, c.v_scale), before):
+            assert torch.equal(R.bits(x[dst, h]), R.bits(y[src, h]))
+        assert torch.equal(acc[0, h, :budget], acc0[0, h, keep])
+    short = c.slots(1, torch.arange(budget // 2))
+    for x, y in zip((c.k, c.v, c.k_scale, c.v_scale), before):
+        assert torch.equal(R.bits(x[short]), R.bits(y[short]))
+
+
 # ---------------------------------------------------------------- rope
 ROPES = [
     ("bf16", 2, 4, 128, 64, 128, False, {}),
@@ -482,6 +503,61 @@ def test_rope_is_relative():
         dots.append(float((r.double() * rk.double()).sum()))
     size = float((q.abs() * k.abs()).sum())
     assert max(dots) - min(dots) <= 4 * size * 2.0 ** -20  # twice two roundings of sine, cosine and products each
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3", "f32"])
+def test_calls_captured_and_replayed(dtype):
+    """One graph of all five calls, replayed on other inputs, leaves what the calls leave one by one."""
+    hkv, G, d, N, B = 2, 4, 128, 5, 3
+    def state(seed):
+        c = R.PagedCache(dtype, [400, 77, 150], hkv, d, 16, seed=seed, poison=False)
+        g = gen(seed)
+        return c, dict(
+            qkv=torch.randn(B, N, hkv * (G + 2), d, device="cuda", generator=g).to(R.q_dtype(dtype)),
+            pos=torch.randint(0, 5000, (B, N), device="cuda", generator=g, dtype=torch.int32), new=i32([5, 3, 1]),
+            words=torch.tensor(signed([mask_words(random_tree(N, seed + b)) for b in range(B)]), device="cuda"),
+            path=torch.randint(0, 5, (B, N), device="cuda", generator=g, dtype=torch.int32), plen=i32([3, 2, 1]),
+            acc=torch.rand(B, hkv, c.cap, device="cuda", generator=g), out=torch.zeros(B, N, hkv * G, d, device="cuda", dtype=R.q_dtype(dtype)),
+            q_out=torch.zeros(B, N, hkv * G, d, device="cuda", dtype=R.q_dtype(dtype)), lens1=torch.zeros_like(c.lens),
+            lens2=torch.zeros_like(c.lens), kept=torch.zeros(B, hkv, 90, dtype=torch.int32, device="cuda"),
+            o1=torch.zeros(B, hkv * G, d, device="cuda", dtype=R.q_dtype(dtype)))
+    table = hs2.rope_table(64)
+
+    def step(c, s, ws_tree, ws_full):
+        x, hq = s["qkv"], hkv * G
+        hs2.rope_append(x[:, :, :hq], x[:, :, hq:hq + hkv], x[:, :, hq + hkv:], s["pos"], table, c.k, c.v, c.lens,
+                        num_new=s["new"], q_out=s["q_out"], **c.kw())
+        hs2.tree_attn(s["q_out"], c.k, c.v, c.lens, tree_mask=s["words"], num_draft=s["new"], out=s["out"], workspace=ws_tree, **c.kw())
+        hs2.tree_accept(c.k, c.v, c.lens, s["path"], s["plen"], num_draft=s["new"], lens_out=s["lens1"], **c.kw())
+        hs2.full_attn_accumulate(s["o1"], c.k, c.v, s["lens1"], s["acc"], decay=0.5, out=s["o1"].clone(), workspace=ws_full, **c.kw())
+        hs2.cache_evict(c.k, c.v, s["lens1"], s["acc"], 90, 10, kept=s["kept"], lens_out=s["lens2"], **c.kw())
+
+    c, s = state(3)
+    ws_tree = hs2.alloc_tree_workspace(s["q_out"], c.k)
+    ws_full = hs2.alloc_workspace(B, hkv, G, d, c.cap)
+    first = c.snapshot() + [x.clone() for x in s.values()]
+    step(c, s, ws_tree, ws_full)  # the kernels are loaded before the capture
+    live = [x for x in (c.k, c.v, c.k_scale, c.v_scale)] + list(s.values())
+    for x, y in zip(live, first):
+        if x is not None:
+            x.copy_(y)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(c, s, ws_tree, ws_full)
+    for seed in (4, 5):
+        other, t = state(seed)
+        c.lens.copy_(other.lens)
+        if c.table is not None:
+            c.table.copy_(other.table)
+        for x, y in zip(live, [other.k, other.v, other.k_scale, other.v_scale] + list(t.values())):
+            if x is not None:
+                x.copy_(y)
+        g.replay()
+        step(other, t, hs2.alloc_tree_workspace(t["q_out"], other.k), hs2.alloc_workspace(B, hkv, G, d, other.cap))
+        torch.cuda.synchronize()
+        for x, y in zip(live, [other.k, other.v, other.k_scale, other.v_scale] + list(t.values())):
+            assert x is None or torch.equal(R.bits(x), R.bits(y))
+    assert hs2.workspace_status(ws_tree) == hs2.OK and hs2.workspace_status(ws_full) == hs2.OK
 
 
 # ---------------------------------------------------------------- together
