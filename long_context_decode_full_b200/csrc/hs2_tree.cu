@@ -227,13 +227,11 @@ __global__ void __launch_bounds__(32 * kCombineWarps) tree_combine_kernel(const 
   griddep_launch_dependents();
   const int kvh = blockIdx.y, b = blockIdx.z, lane = threadIdx.x & 31;
   const int row0 = blockIdx.x / (D / 32) * 32, col4 = blockIdx.x % (D / 32) * kCombineWarps + (threadIdx.x >> 5);
-  const int T = tree_len(p, b), n = tree_drafts(p, b, T);
-  if (row0 >= n * p.G) return;
-  const int64_t total = (int64_t)p.Hkv * p.prefix[p.B];
-  const int nb = p.prefix[b + 1] - p.prefix[b];
-  if (nb == 0) return;
+  const int T = tree_len(p, b), n = tree_drafts(p, b, T), before = p.prefix[b], nb = p.prefix[b + 1] - before;
+  const int64_t total = (int64_t)p.Hkv * p.prefix[p.B];  // all fetched together
+  if (row0 >= n * p.G || nb == 0) return;
   const TreeShare share(total, p.groups);
-  const int64_t U0 = (int64_t)p.Hkv * p.prefix[b] + (int64_t)kvh * nb;
+  const int64_t U0 = (int64_t)p.Hkv * before + (int64_t)kvh * nb;
   const int64_t c0 = share.owner(U0), c1 = share.owner(U0 + nb - 1);
   // 32 rows lie in one block, and in one stream's rows
   const int per_block = p.rows * p.streams, block = row0 / per_block, in_block = row0 % per_block;

@@ -38,8 +38,11 @@ __device__ __forceinline__ int tree_len(const TreeParams &p, int b) {
   return clamp_len(__ldg(p.seq_lens + b), (int)p.t_cap);
 }
 // drafted tokens of sequence b, the last n of its T rows
+__device__ __forceinline__ int tree_given_drafts(const TreeParams &p, int b) {
+  return p.num_draft ? __ldg(p.num_draft + b) : p.N;
+}
 __device__ __forceinline__ int tree_drafts(const TreeParams &p, int b, int T) {
-  return clamp_len(p.num_draft ? __ldg(p.num_draft + b) : p.N, min(p.N, T));
+  return clamp_len(tree_given_drafts(p, b), min(p.N, T));
 }
 // the drafts that token i of sequence b sees
 __device__ __forceinline__ uint64_t tree_bits(const TreeParams &p, int b, int i, int n) {

@@ -113,6 +113,7 @@ struct TreeWalk {
   __device__ __forceinline__ bool next(const TreeParams &p, int block, TreeSeg &s) {
     while (g < g1 && b < p.B) {
       s.T = tree_len(p, b);
+      const int given = tree_given_drafts(p, b);  // fetched together
       const int nb = (s.T + kKeys - 1) / kKeys, r = g - base;
       if ((int64_t)r >= (int64_t)p.Hkv * nb) {
         base += p.Hkv * nb;
@@ -123,7 +124,7 @@ struct TreeWalk {
       s.kvh = r / nb;
       s.i0 = r - s.kvh * nb;
       s.i1 = min(nb, s.i0 + (g1 - g));
-      const int n = tree_drafts(p, b, s.T);
+      const int n = clamp_len(given, min(p.N, s.T));
       s.first = s.T - n;
       s.special0 = max(s.i0, min(s.i1, s.first / kKeys));
       s.begins = g == g0;
@@ -384,7 +385,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tensormap(&tmk);
     prefetch_tensormap(&tmv);
   }
+  if (warp == 13) {
+    tc::tmem_alloc(&info->tmem, kTmemCols);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before();
   __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = info->tmem;
   griddep_wait();
   griddep_launch_dependents();
   if (warp == 0) {  // the tiles of all sequences, then the sequence where the share begins
@@ -421,15 +429,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (blockIdx.x == 0) tree_prefix(p, p.prefix);
   }
   __syncthreads();
-  if (info->g0 >= info->g1) return;  // no tiles for this CTA
-  if (warp == 13) {
-    tc::tmem_alloc(&info->tmem, kTmemCols);
-    tc::tmem_relinquish();
+  if (info->g0 >= info->g1) {  // no tiles for this CTA
+    if (warp == 13) tc::tmem_dealloc(tmem, kTmemCols);
+    return;
   }
-  tc::fence_before();
-  __syncthreads();
-  tc::fence_after();
-  const uint32_t tmem = info->tmem;
   TreeWalk walk(*info);
   TreeSeg seg;
   const int wg = warp >> 2;
