@@ -84,7 +84,8 @@ struct TreeTc {
   static constexpr int kSlots = 2;   // tiles in the values warpgroup's hands
   static constexpr int kScales = 8;  // tiles whose scales are there or on the way: their fetch takes longer than a tile's logits
   static constexpr size_t oStage = 2 * kQ, oVals = oStage + (size_t)kStages * kTile, oScale = oVals + kSlots * kVals,
-                          oBar = oScale + (FP8 ? kScales * 2 * kKeys * 4 : 0);
+                          oQScale = oScale + (FP8 ? kScales * 2 * kKeys * 4 : 0),
+                          oBar = oQScale + (FP8 ? 2 * kStreamRows * 4 : 0);
   // p_full and o_full: a stream's halves of a tile
   // full[S], empty[S], q_full[2], s_full[2], p_full[2][2], o_full[2][2], and per slot v_ready, v_free, v_landed; scale_full[8], scale_free[8]; done
   static constexpr int kBars = 2 * kStages + 12 + 3 * kSlots + 2 * kScales + 1;
@@ -461,55 +462,73 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tok = r / p.G, head = seg.kvh * p.G + r % p.G;
       const uint64_t bits = mine ? tree_bits(p, seg.b, tok, n) : 0ull;
       float c2 = p.c2;
-      // the query row to shared memory, 128-byte swizzle
-      if (mine) {
-        const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) +
-                                                           ((int64_t)seg.b * p.N + tok) * p.q_stride + (int64_t)head * D);
-        uint4 x[D / 8];
+      // the query rows to shared memory, 128-byte swizzle
+      if constexpr (!FP8) {
+        if (mine) {
+          const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) +
+                                                             ((int64_t)seg.b * p.N + tok) * p.q_stride + (int64_t)head * D);
+          uint4 x[D / 8];
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) x[c] = __ldg(src + c);
-        if constexpr (!FP8) {
+          for (int c = 0; c < D / 8; ++c) x[c] = __ldg(src + c);
 #pragma unroll
           for (int c = 0; c < D / 8; ++c)
             *reinterpret_cast<uint4 *>(sq + (c >> 3) * (kStreamRows * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = x[c];
-        } else {
+        }
+      } else {
+        // eight neighbouring threads split a row into its terms, 16 elements each, and the row's own thread takes its scale
+        constexpr int kPer = D / 16;
+        const int r_first = block * 2 * kStreamRows + (seg.pair ? s * kStreamRows : 0);
+        const int rows = min(kStreamRows, n * p.G - r_first), c = lane % kPer;
+        float *scales = reinterpret_cast<float *>(smem + C::oQScale) + s * kStreamRows;
+#pragma unroll 1
+        for (int y = (tid & 127) / kPer; y < ((rows + 3) & ~3); y += 128 / kPer) {  // the same number of rounds for a warp
+          const int rr = r_first + min(y, rows - 1), hh = seg.kvh * p.G + rr % p.G;
+          const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) +
+                                                             ((int64_t)seg.b * p.N + rr / p.G) * p.q_stride + (int64_t)hh * D) + 2 * c;
+          const uint4 x0 = __ldg(src), x1 = __ldg(src + 1);
+          const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
           float top = 0.f;
           bool finite = true;
-          const uint32_t *w = reinterpret_cast<const uint32_t *>(x);
 #pragma unroll
-          for (int e = 0; e < D / 2; ++e) {
+          for (int e = 0; e < 8; ++e) {
             const float a = fabsf(bf16_lo(w[e])), b = fabsf(bf16_hi(w[e]));
             top = fmaxf(top, fmaxf(a, b));
             finite = finite && a <= 3.4e38f && b <= 3.4e38f;
+          }
+#pragma unroll
+          for (int o = kPer / 2; o; o >>= 1) {
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            finite = __shfl_xor_sync(0xffffffffu, (int)finite, o) && finite;
           }
           // the largest power of two that takes the row to at most 448
           const uint32_t tb = __float_as_uint(top);
           const int k = min(126, 8 + 127 - (int)(tb >> 23) - ((tb & 0x7FFFFFu) > 0x600000u));
           const float up = __uint_as_float((uint32_t)(k + 127) << 23);
-          c2 = finite ? p.c2 * __uint_as_float((uint32_t)(127 - k) << 23) : __int_as_float(0x7FC00000);
+          uint32_t hi[4], lo[4];
 #pragma unroll
-          for (int c = 0; c < D / 16; ++c) {  // 16 codes of each term
-            uint32_t hi[4], lo[4];
+          for (int e = 0; e < 4; ++e) {
+            hi[e] = lo[e] = 0;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              hi[e] = lo[e] = 0;
-#pragma unroll
-              for (int f = 0; f < 2; ++f) {
-                const uint32_t u = w[8 * c + 2 * e + f];
-                const float2 v = make_float2(bf16_lo(u) * up, bf16_hi(u) * up);
-                const uint32_t h = __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
-                const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)h, __NV_E4M3);
-                const float2 back = __half22float2(*reinterpret_cast<const __half2 *>(&hr));
-                const uint32_t l = __nv_cvt_float2_to_fp8x2(make_float2(v.x - back.x, v.y - back.y), __NV_SATFINITE, __NV_E4M3);
-                hi[e] |= h << (16 * f);
-                lo[e] |= l << (16 * f);
-              }
+            for (int f = 0; f < 2; ++f) {
+              const uint32_t u = w[2 * e + f];
+              const float2 v = make_float2(bf16_lo(u) * up, bf16_hi(u) * up);
+              const uint32_t h = __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+              const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)h, __NV_E4M3);
+              const float2 back = __half22float2(*reinterpret_cast<const __half2 *>(&hr));
+              const uint32_t l = __nv_cvt_float2_to_fp8x2(make_float2(v.x - back.x, v.y - back.y), __NV_SATFINITE, __NV_E4M3);
+              hi[e] |= h << (16 * f);
+              lo[e] |= l << (16 * f);
             }
-            uint8_t *dst = sq + row * 128 + ((c ^ (row & 7)) << 4);
+          }
+          if (y < rows) {
+            uint8_t *dst = sq + y * 128 + ((c ^ (y & 7)) << 4);
             *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
             *reinterpret_cast<uint4 *>(dst + kStreamRows * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            if (c == 0) scales[y] = finite ? p.c2 * __uint_as_float((uint32_t)(127 - k) << 23) : __int_as_float(0x7FC00000);
           }
         }
+        asm volatile("bar.sync %0, 128;" ::"r"(4 + s) : "memory");
+        if (mine) c2 = scales[row];
       }
       __syncwarp();
       {
@@ -595,19 +614,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                     x[e] = u.x, x[e + 1] = u.y;
                   }
                 }
-                const uint32_t see = (uint32_t)(seen >> c);
+                if (special) {
+                  const uint32_t see = (uint32_t)(seen >> c);
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  if (!((see >> e) & 1u)) x[e] = -INFINITY;
+                  for (int e = 0; e < 32; ++e)
+                    if (!((see >> e) & 1u)) x[e] = -INFINITY;
+                }
               };
-              float top = -INFINITY;
+              float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
               for (int c = 0; c < 64; c += 32) {
                 float x[32];
                 load_logits(c, x);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) top = fmaxf(top, x[e]);
+                for (int e = 0; e < 32; e += 8)
+#pragma unroll
+                  for (int f = 0; f < 4; ++f) mx[f] = fmaxf(fmaxf(mx[f], x[e + f]), x[e + f + 4]);
               }
+              const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
               float alpha = 1.f;
               if (m == -INFINITY ? top > -INFINITY : top > m + growth) {
                 alpha = m == -INFINITY ? 0.f : ex2_approx((m - top) * c2);
@@ -617,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               __syncwarp();
               if (any_product && (bad_here || __any_sync(0xffffffffu, alpha != 1.f))) rescale(alpha);
               const float shift = m == -INFINITY ? 0.f : -m * c2;  // nothing seen yet: weights 0
-              sum = 0.f;
+              float2 sums = make_float2(0.f, 0.f);
 #pragma unroll
               for (int c = 0; c < 64; c += 32) {
                 float x[32];
@@ -626,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) {
                   float2 a = make_float2(ex2_approx(fmaf(x[e], c2, shift)), ex2_approx(fmaf(x[e + 1], c2, shift)));
-                  sum += a.x + a.y;
+                  sums = add2(sums, a);
                   if constexpr (FP8) {  // a scale that is not seen may be anything
                     a = mul2(a, lds_float2(vs + 64 * h + c + e));
                     a.x = (see >> e) & 1u ? a.x : 0.f;
@@ -635,6 +659,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   w[(c + e) >> 1] = pack_bf16(a.x, a.y);
                 }
               }
+              sum = sums.x + sums.y;
             }
             l += sum;
             tmem_st32(tx, w);
@@ -764,18 +789,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait_or_abort(full + ring.stage, ring.parity, abort, p.err, kErrFullWait);
         uint8_t *tile = smem + C::oStage + (size_t)ring.stage * C::kTile;
         bool bad = false;
-        if (draft) {  // whole rows
+        if (draft) {  // the largest magnitude of the row's codes: NaN (E4M3), infinity and NaN (bf16) lie above all others
+          uint32_t top = 0;
+#pragma unroll
           for (int c = 0; c < C::kPanels * 8; ++c) {
             uint32_t w[4];
             lds128(w, smem_u32(tile) + (c >> 3) * C::kPanel + r * 128 + (c & 7) * 16);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              if constexpr (FP8)  // a byte of 0x7F but for the sign: NaN
-                bad = bad || __vcmpeq4(w[e] & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0u;
-              else  // an exponent of ones: infinity or NaN
-                bad = bad || (w[e] & 0x7F80u) == 0x7F80u || (w[e] & 0x7F800000u) == 0x7F800000u;
+              if constexpr (FP8) top = __vmaxu4(top, w[e] & 0x7F7F7F7Fu);
+              else top = __vmaxu2(top, w[e] & 0x7FFF7FFFu);
             }
           }
+          if constexpr (FP8) bad = __vcmpeq4(top, 0x7F7F7F7Fu) != 0u;
+          else bad = __vcmpgeu2(top, 0x7F807F80u) != 0u;
         }
         const bool clear = !live || bad;
         if (seg.i0 + i >= seg.special0) {  // the mask is clear, and every row has been looked at
@@ -801,6 +828,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         } else if (clear) {
+#pragma unroll
           for (int c = 0; c < C::kPanels * 8; ++c)
             *reinterpret_cast<uint4 *>(tile + (c >> 3) * C::kPanel + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
         }
