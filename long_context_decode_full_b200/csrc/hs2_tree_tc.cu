@@ -43,16 +43,17 @@
 // and the SM clock falls to 1.1-1.6 GHz, so work that is not needed costs time even
 // where it is hidden: blocks of at most 64 rows take M = 64 products (8 drafts over
 // 256K x 4 sequences, bf16: 404 -> 371 us; 5.8 TB/s), and weights need no maximum.
-//   8 x 8 rows, 4 x 262,144 tokens, bf16    371 us sustained (a launch alone 323 us: memory)
-//   64 x 8 rows, 8 x 32,768, bf16           326 us sustained (a launch alone 280 us), 0.77 PFLOP/s
-//   16 x 8 rows, 1 x 1,048,576, E4M3        438 us sustained (a launch alone 373 us)
+//   8 x 8 rows, 4 x 262,144 tokens, bf16    355 us sustained (a launch alone 323 us: memory)
+//   64 x 8 rows, 8 x 32,768, bf16           313 us sustained, 0.81 PFLOP/s
+//   16 x 8 rows, 1 x 1,048,576, E4M3        419 us sustained (a launch alone 360 us)
 // The last two are bound by a stream's chain: logits product, exponentials, weights'
 // product, about 3,500 cycles per tile of both streams where the products need 2,048.
-// Measured and dropped (us, in this order of cases): tiles of 64 positions with two
+// Measured and dropped, against 371 / 326 / 440 at that step (us, in this order of
+// cases; boxes differ by up to 10%): tiles of 64 positions with two
 // sets of logits columns 449 / 341 / 609 (a step with N = 64 takes as long as one with
 // N = 128); two warpgroups per stream 399 / 317 / 498; two passes, maximum first,
 // 397 / 315 / 640; a quarter of the exponentials as a polynomial on the FMA units
-// 406 / 326 / 456.
+// 406 / 326 / 456; eight conversion warps (E4M3) 460.
 #include <type_traits>
 
 #include "hs2.h"
