@@ -49,7 +49,7 @@
 // The last two are bound by a stream's chain: logits product, exponentials, weights'
 // product, about 3,500 cycles per tile of both streams where the products need 2,048.
 // Measured and dropped, against 371 / 326 / 440 at that step (us, in this order of
-// cases; boxes differ by up to 10%): tiles of 64 positions with two
+// cases; cards differ by up to 10%): tiles of 64 positions with two
 // sets of logits columns 449 / 341 / 609 (a step with N = 64 takes as long as one with
 // N = 128); two warpgroups per stream 399 / 317 / 498; two passes, maximum first,
 // 397 / 315 / 640; a quarter of the exponentials as a polynomial on the FMA units
