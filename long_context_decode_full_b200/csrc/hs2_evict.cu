@@ -104,7 +104,9 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_kernel(const AcceptPara
 // writes its positions behind the earlier shares' counts.  A pass counts into shared
 // memory; each CTA adds its part of the bins over the cluster and hands the sums to
 // all (distributed shared memory), so every CTA finds the bin itself.  A share's
-// keys stay in registers where they fit.  Bound by seven cluster barriers: 27 us for
+// keys stay in registers where they fit; a unit of one CTA needs no cluster.  Up to
+// 1,024 positions are ranked by counting instead, each thread's key against all.
+// Bound by seven cluster barriers: 27 us for
 // 16 units of 65,536 (37 us with one warp vote per key, which takes ~190 cycles, and
 // keys read again in every pass).
 constexpr int kPickThreads = 1024;
@@ -119,7 +121,7 @@ __device__ __forceinline__ uint32_t sum_key(float x) {
 }
 
 __global__ void __launch_bounds__(kPickThreads) pick_kernel(const EvictParams p) {
-  __shared__ uint32_t sh_hist[kPickBins], sh_tot[kPickBins];
+  __shared__ __align__(16) uint32_t sh_hist[kPickBins], sh_tot[kPickBins];
   __shared__ int sh_warp[33], sh_res[2];
   __shared__ int2 sh_counts[8];
   cg::cluster_group cluster = cg::this_cluster();
@@ -139,6 +141,39 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const EvictParams p)
   const float *acc = p.acc + (int64_t)u * p.acc_stride;
   for (int i = rank * kPickThreads + tid; i < W; i += C * kPickThreads) kept[take + i] = n + i;
   if (take == 0) return;
+  if (n <= kPickThreads) {  // the same for the cluster
+    if (rank != 0) return;
+    const uint32_t key = tid < n ? sum_key(__ldg(acc + tid)) : 0u;
+    sh_tot[tid] = key;
+    __syncthreads();
+    // sums before this one: larger ones, and equal ones at lower positions
+    const uint4 *all = reinterpret_cast<const uint4 *>(sh_tot);
+    const int mine = tid / 32 * 8, end = (n + 3) / 4;  // the warp's own keys
+    int before = 0;
+    for (int j = 0; j < min(mine, end); ++j) {
+      const uint4 x = all[j];
+      before += (x.x >= key) + (x.y >= key) + (x.z >= key) + (x.w >= key);
+    }
+    for (int j = mine; j < min(mine + 8, end); ++j) {
+      const uint4 x = all[j];
+      const int t = 4 * j;
+      before += (x.x > key || (x.x == key && t < tid)) + (x.y > key || (x.y == key && t + 1 < tid)) +
+                (x.z > key || (x.z == key && t + 2 < tid)) + (x.w > key || (x.w == key && t + 3 < tid));
+    }
+    for (int j = mine + 8; j < end; ++j) {
+      const uint4 x = all[j];
+      before += (x.x > key) + (x.y > key) + (x.z > key) + (x.w > key);
+    }
+    const bool taken = tid < n && before < take;
+    int tot;
+    const int at = block_exclusive_scan(taken, sh_warp, &tot);
+    if (taken) kept[at] = tid;
+    return;
+  }
+  auto meet = [&]() {
+    if (C == 1) __syncthreads();
+    else cluster.sync();
+  };
   const int share = (n + C - 1) / C, c0 = min(n, rank * share), c1 = min(n, c0 + share);
   const bool held = share <= kPickKeys * kPickThreads;
   uint32_t keys[kPickKeys];
@@ -175,18 +210,20 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const EvictParams p)
         for (int k = 0; k < kLoads; ++k) count(t0 + k * kPickThreads + tid, sum_key(x[k]));
       }
     }
-    cluster.sync();
-    const int per = nb / C;  // C is a power of two up to 8
-    for (int i = tid; i < per; i += kPickThreads) {
-      uint32_t sum = 0;
+    meet();
+    if (C > 1) {
+      const int per = nb / C;  // C is a power of two up to 8
+      for (int i = tid; i < per; i += kPickThreads) {
+        uint32_t sum = 0;
 #pragma unroll 4
-      for (int r = 0; r < C; ++r) sum += cluster.map_shared_rank(sh_hist, r)[rank * per + i];
+        for (int r = 0; r < C; ++r) sum += cluster.map_shared_rank(sh_hist, r)[rank * per + i];
 #pragma unroll 4
-      for (int r = 0; r < C; ++r) cluster.map_shared_rank(sh_tot, r)[rank * per + i] = sum;
+        for (int r = 0; r < C; ++r) cluster.map_shared_rank(sh_tot, r)[rank * per + i] = sum;
+      }
+      cluster.sync();
     }
-    cluster.sync();
     int above;
-    const int bin = find_threshold_bin(sh_tot, nb, need, &above, sh_warp, sh_res);
+    const int bin = find_threshold_bin(C > 1 ? sh_tot : sh_hist, nb, need, &above, sh_warp, sh_res);
     prefix |= (uint32_t)bin << shift;
     need -= above;
   }
@@ -219,7 +256,7 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const EvictParams p)
     block_exclusive_scan(eq, sh_warp, &tot_eq);
   }
   if (tid < C) cluster.map_shared_rank(sh_counts, tid)[rank] = make_int2(tot_gt, tot_eq);
-  cluster.sync();
+  meet();
   int gt0 = 0, eq0 = 0;
   for (int r = 0; r < rank; ++r) {
     gt0 += sh_counts[r].x;

@@ -311,7 +311,7 @@ def test_full_attn_accumulate(dtype, hkv, G, d, page, decay, fresh):
 # ---------------------------------------------------------------- evict
 @pytest.mark.parametrize("dtype,hkv,d,page,budget,window", [
     ("bf16", 2, 128, 64, 100, 16), ("e4m3", 3, 128, 16, 333, 128), ("f32", 1, 64, 0, 1, 0), ("bf16", 2, 64, 32, 64, 64),
-    ("bf16", 1, 128, 64, 2000, 7), ("e4m3", 1, 128, 0, 1023, 0)])
+    ("bf16", 1, 128, 64, 2000, 7), ("e4m3", 1, 128, 0, 1023, 0), ("bf16", 2, 64, 16, 690, 3)])
 def test_cache_evict(dtype, hkv, d, page, budget, window):
     lens = [5000, 99, 0, budget, budget + 1, 2100, 700]
     c = R.PagedCache(dtype, lens, hkv, d, page, seed=11)
