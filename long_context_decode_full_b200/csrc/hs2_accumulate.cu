@@ -98,6 +98,226 @@ __global__ void __launch_bounds__(kAccThreads) accumulate_kernel(const Accumulat
   }
 }
 
+// ------------------------------------------------------------------ fp32 caches
+// The attention of the call over an fp32 cache: logits and segment records as
+// full_attn_f32_kernel leaves them (the same shares of 64-position tiles).  A warp
+// takes 8 rows of every tile for all heads of the group: a lane has D / 32
+// neighbouring dimensions, so a row of K or V is one 512- or 256-byte load; the
+// 8 G products' partial sums are added over the lanes by halving exchanges and
+// passed to all lanes through shared memory; the warps' sums are joined at a
+// segment's end.  Bound by reading K and V (8 warps of 8 rows: 64 KB per CTA on the
+// way).  One warp per head, as in that kernel, leaves most of an SM idle for small
+// groups: 10 sequences of up to 17,430 tokens, 8 kv heads of one query head, d 128,
+// take 140 us with the update (525 us with that kernel; the bytes' floor is 111).
+constexpr int kRowWarps = 8, kRowTile = 64, kWarpRows = kRowTile / kRowWarps;
+
+template <int N>
+struct RowVec {
+  float x[N];
+  __device__ __forceinline__ void load(const float *p) {
+    if constexpr (N == 4) {
+      const float4 v = __ldg(reinterpret_cast<const float4 *>(p));
+      x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+    } else {
+      const float2 v = __ldg(reinterpret_cast<const float2 *>(p));
+      x[0] = v.x, x[1] = v.y;
+    }
+  }
+};
+
+// Sums of N values over the 32 lanes: halves are exchanged while there are two or
+// more, so value i ends in the lanes whose upper log2 N bits are i (N <= 32), or in
+// the lane i / (N / 32), N / 32 values each.
+template <int N>
+__device__ __forceinline__ void sum_over_lanes(float *x, int lane) {
+  int o = 16;
+#pragma unroll
+  for (int n = N; n > 1 && o > 0; n >>= 1, o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < n / 2; ++i) {
+      const float give = up ? x[i] : x[i + n / 2], keep = up ? x[i + n / 2] : x[i];
+      x[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+    }
+  }
+  for (; o > 0; o >>= 1) x[0] += __shfl_xor_sync(0xffffffffu, x[0], o);
+}
+
+template <int G, int D>
+__global__ void __launch_bounds__(32 * kRowWarps) rows_attn_f32_kernel(const FullParams p) {
+  extern __shared__ int32_t sh_prefix[];
+  __shared__ __align__(16) float sh_s[kRowWarps][kWarpRows * G];
+  __shared__ float sh_m[kRowWarps][G], sh_l[kRowWarps][G], sh_o[kRowWarps][G * D];
+  constexpr int NV = D / 32, NS = kWarpRows * G;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  griddep_wait();
+  griddep_launch_dependents();
+  if (warp == 0) {
+    int carry = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+      const int b = b0 + lane;
+      int x = b < p.B ? (clamp_len(__ldg(p.seq_lens + b), (int)p.t_cap) + kRowTile - 1) / kRowTile : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (b < p.B) sh_prefix[b + 1] = carry + x;
+      carry += __shfl_sync(0xffffffffu, x, 31);
+    }
+    if (lane == 0) sh_prefix[0] = 0;
+  }
+  __syncthreads();
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i <= p.B; i += 32 * kRowWarps) p.ws.prefix[i] = sh_prefix[i];
+  const int64_t total = (int64_t)p.Hkv * sh_prefix[p.B];
+  if (total == 0) return;
+  const Partition part{total, p.N};
+  const int64_t g1 = part.start(blockIdx.x + 1);
+  const float cl = p.c * 1.4426950408889634f;
+  for (int64_t g = part.start(blockIdx.x); g < g1;) {
+    int lo = 0, hi = p.B - 1;  // the sequence of tile g
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if ((int64_t)p.Hkv * sh_prefix[mid] <= g) lo = mid;
+      else hi = mid - 1;
+    }
+    const int b = lo, nb = sh_prefix[b + 1] - sh_prefix[b];
+    const int64_t r = g - (int64_t)p.Hkv * sh_prefix[b];
+    const int kvh = (int)(r / nb), i0 = (int)(r % nb), i1 = (int)min((int64_t)nb, i0 + (g1 - g));
+    const int64_t u = (int64_t)b * p.Hkv + kvh, U = (int64_t)p.Hkv * sh_prefix[b] + (int64_t)kvh * nb;
+    g += i1 - i0;
+    const int T = clamp_len(__ldg(p.seq_lens + b), (int)p.t_cap);
+    RowVec<NV> q[G];
+    float m[G], l[G], o[G][NV];
+#pragma unroll
+    for (int h = 0; h < G; ++h) {
+      q[h].load(static_cast<const float *>(p.q) + (u * G + h) * D + lane * NV);
+      m[h] = -INFINITY, l[h] = 0.f;
+#pragma unroll
+      for (int e = 0; e < NV; ++e) o[h][e] = 0.f;
+    }
+    for (int i = i0; i < i1; ++i) {
+      const int t0 = i * kRowTile + warp * kWarpRows;
+      int64_t mine = -1;  // lane's row's place
+      if (lane < kWarpRows && t0 + lane < T) {
+        const int pos = t0 + lane;
+        mine = p.page_table == nullptr ? (int64_t)b * p.page_size + pos
+                                       : (int64_t)__ldg(p.page_table + (int64_t)b * p.max_pages + pos / p.page_size) * p.page_size +
+                                             pos % p.page_size;
+        if (mine < 0 || mine >= p.num_slots) mine = -1;
+      }
+      RowVec<NV> k[kWarpRows], v[kWarpRows];
+#pragma unroll
+      for (int j = 0; j < kWarpRows; ++j) {
+        const int64_t slot = __shfl_sync(0xffffffffu, mine, j);
+        if (slot >= 0) {
+          const int64_t at = (slot * p.Hkv + kvh) * D + lane * NV;
+          k[j].load(static_cast<const float *>(p.k) + at);
+          v[j].load(static_cast<const float *>(p.v) + at);
+        } else {
+#pragma unroll
+          for (int e = 0; e < NV; ++e) k[j].x[e] = v[j].x[e] = 0.f;
+        }
+      }
+      float s[NS];
+#pragma unroll
+      for (int j = 0; j < kWarpRows; ++j)
+#pragma unroll
+        for (int h = 0; h < G; ++h) {
+          float a = 0.f;
+#pragma unroll
+          for (int e = 0; e < NV; ++e) a = fmaf(q[h].x[e], k[j].x[e], a);
+          s[j * G + h] = a;
+        }
+      sum_over_lanes<NS>(s, lane);
+      constexpr int kPer = NS >= 32 ? NS / 32 : 1, kShare = NS >= 32 ? 1 : 32 / NS;  // sums of a lane, lanes of a sum
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) {
+        const int at = lane / kShare * kPer + e, j = at / G;
+        if (lane % kShare == 0) {
+          sh_s[warp][at] = t0 + j < T ? s[e] : -INFINITY;
+          if (t0 + j < T) p.ws.logits[(u * p.ustride + t0 + j) * G + at % G] = s[e];
+        }
+      }
+      __syncwarp();
+#pragma unroll
+      for (int e = 0; e < NS; e += 4) {
+        const float4 x = *reinterpret_cast<const float4 *>(&sh_s[warp][e]);
+        s[e] = x.x, s[e + 1] = x.y, s[e + 2] = x.z, s[e + 3] = x.w;
+      }
+      __syncwarp();
+#pragma unroll
+      for (int h = 0; h < G; ++h) {
+        float top = m[h];
+#pragma unroll
+        for (int j = 0; j < kWarpRows; ++j) top = fmaxf(top, s[j * G + h]);
+        const float at = top == -INFINITY ? 0.f : top, alpha = m[h] == top ? 1.f : exp2f((m[h] - at) * cl);
+        m[h] = top;
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < kWarpRows; ++j) {
+          s[j * G + h] = exp2f((s[j * G + h] - at) * cl);
+          sum += s[j * G + h];
+        }
+        l[h] = fmaf(l[h], alpha, sum);
+#pragma unroll
+        for (int e = 0; e < NV; ++e) {
+          float a = o[h][e] * alpha;
+#pragma unroll
+          for (int j = 0; j < kWarpRows; ++j) a = fmaf(s[j * G + h], v[j].x[e], a);
+          o[h][e] = a;
+        }
+      }
+    }
+    // the warps' sums to the segment's record
+#pragma unroll
+    for (int h = 0; h < G; ++h) {
+      if (lane == 0) sh_m[warp][h] = m[h], sh_l[warp][h] = l[h];
+#pragma unroll
+      for (int e = 0; e < NV; ++e) sh_o[warp][h * D + lane * NV + e] = o[h][e];
+    }
+    __syncthreads();
+    const int64_t rec_at = blockIdx.x - part.cfirst(U);
+    if (rec_at < 0 || rec_at >= p.R) {
+      if (threadIdx.x == 0) set_error(p.ws.err, kErrRecord);
+    } else {
+      float *rec = p.ws.records + (size_t)(u * p.R + rec_at) * G * (D + 2);
+      for (int e = threadIdx.x; e < G * D; e += 32 * kRowWarps) {
+        const int h = e / D;
+        float M = -INFINITY, L = 0.f, O = 0.f;
+#pragma unroll
+        for (int w = 0; w < kRowWarps; ++w) M = fmaxf(M, sh_m[w][h]);
+        const float at = M == -INFINITY ? 0.f : M;
+#pragma unroll
+        for (int w = 0; w < kRowWarps; ++w) {
+          const float f = exp2f((sh_m[w][h] - at) * cl);
+          L = fmaf(f, sh_l[w][h], L);
+          O = fmaf(f, sh_o[w][e], O);
+        }
+        if (e % D == 0) rec[h] = M, rec[G + h] = L;
+        rec[2 * G + e] = O;
+      }
+    }
+    __syncthreads();  // shared memory is free for the next segment
+  }
+}
+
+template <int D>
+cudaError_t run_rows(const FullParams &p, int grid, cudaStream_t s) {
+  const size_t smem = (size_t)(p.B + 1) * 4;
+  auto go = [&](auto kern) {
+    const cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kern), (kMaxBatchSmem + 1) * 4);
+    return e != cudaSuccess ? e : launch_ex(kern, dim3(grid), dim3(32 * kRowWarps), smem, s, 0, p);
+  };
+  switch (p.G) {
+    case 1: return go(rows_attn_f32_kernel<1, D>);
+    case 2: return go(rows_attn_f32_kernel<2, D>);
+    case 4: return go(rows_attn_f32_kernel<4, D>);
+    default: return go(rows_attn_f32_kernel<8, D>);
+  }
+}
+
 template <int D>
 cudaError_t run(const AccumulateParams &p, cudaStream_t s) {
   const ScoreParams &sp = p.sp;
@@ -113,6 +333,11 @@ cudaError_t run(const AccumulateParams &p, cudaStream_t s) {
 }
 
 }  // namespace
+
+cudaError_t launch_rows_f32(const FullParams &p, int grid, cudaStream_t s) {
+  if (p.tile != kRowTile) return cudaErrorInvalidValue;  // the shares that the update reads back
+  return p.D == 64 ? run_rows<64>(p, grid, s) : run_rows<128>(p, grid, s);
+}
 
 cudaError_t launch_accumulate(const AccumulateParams &p, cudaStream_t s) {
   return p.sp.D == 64 ? run<64>(p, s) : run<128>(p, s);

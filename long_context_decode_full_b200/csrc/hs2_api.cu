@@ -519,7 +519,7 @@ int full_attn_select_impl(const hs2_heads *q, const hs2_cache *k_cache, const hs
   if (fuse && (G >= 16) != (cfg.nt == 2))
     return fail(HS2_ERR_UNSUPPORTED, "fused call: no kernel for %d heads per group with %d-head warps", G, 8 * cfg.nt);
   if (!mma) {
-    e = launch_full_f32(p, p.N, s);
+    e = accumulate ? launch_rows_f32(p, p.N, s) : launch_full_f32(p, p.N, s);
     if (e != cudaSuccess) return cuda_fail(e, "full-attention (fp32) launch");
   } else {
     const int box_rows = paged ? (ps < p.tile ? ps : p.tile) : p.tile;

@@ -249,6 +249,8 @@ struct AccumulateParams {
   int32_t fresh;                     // the newest tokens, whose sums start at this call
 };
 cudaError_t launch_accumulate(const AccumulateParams &p, cudaStream_t s);
+// its attention over an fp32 cache, in tiles of full_f32_tile() positions
+cudaError_t launch_rows_f32(const FullParams &p, int grid, cudaStream_t s);
 
 constexpr int kTreeSlots = 3;
 // Attention of drafted tokens over the cache, split over the context.

@@ -278,7 +278,8 @@ def test_tree_accept(dtype, hkv, d, page):
 # ---------------------------------------------------------------- accumulate
 @pytest.mark.parametrize("dtype,hkv,G,d,page,decay,fresh", [
     ("bf16", 2, 8, 128, 64, 0.9, 1), ("e4m3", 1, 16, 128, 32, 1.0, 4), ("f32", 2, 1, 64, 0, 0.0, 0),
-    ("bf16", 1, 32, 64, 16, 0.5, 2 ** 31 - 1), ("f32", 1, 8, 128, 16, 0.75, 3)])
+    ("bf16", 1, 32, 64, 16, 0.5, 2 ** 31 - 1), ("f32", 1, 8, 128, 16, 0.75, 3),
+    ("f32", 3, 2, 128, 48, 0.25, 2), ("f32", 1, 4, 64, 64, 1.0, 1), ("f32", 2, 8, 64, 0, 0.5, 5), ("f32", 5, 1, 128, 16, 0.9, 1)])
 def test_full_attn_accumulate(dtype, hkv, G, d, page, decay, fresh):
     lens = [1, 700, 0, 130, 4099]
     c = R.PagedCache(dtype, lens, hkv, d, page, seed=7)
