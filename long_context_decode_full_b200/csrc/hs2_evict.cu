@@ -105,13 +105,13 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_kernel(const AcceptPara
 // memory; each CTA adds its part of the bins over the cluster and hands the sums to
 // all (distributed shared memory), so every CTA finds the bin itself.  A share's
 // keys stay in registers where they fit; a unit of one CTA needs no cluster.  Up to
-// 1,024 positions are ranked by counting instead, each thread's key against all.
+// 512 positions are ranked by counting instead, each thread's key against all.
 // Bound by seven cluster barriers: 27 us for
 // 16 units of 65,536 (37 us with one warp vote per key, which takes ~190 cycles, and
 // keys read again in every pass).
-constexpr int kPickThreads = 1024;
 constexpr int kPickBins = 2048;
 constexpr int kPickKeys = 16;  // of a thread, in registers
+constexpr int kPickRank = 512;  // positions ranked by counting: n^2 comparisons, 2 us at 512 and 8 at 1,024, where the passes take 8
 
 __device__ __forceinline__ uint32_t sum_key(float x) {
   const uint32_t u = __float_as_uint(x);
@@ -120,6 +120,7 @@ __device__ __forceinline__ uint32_t sum_key(float x) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+template <int kPickThreads>
 __global__ void __launch_bounds__(kPickThreads) pick_kernel(const EvictParams p) {
   __shared__ __align__(16) uint32_t sh_hist[kPickBins], sh_tot[kPickBins];
   __shared__ int sh_warp[33], sh_res[2];
@@ -141,7 +142,7 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const EvictParams p)
   const float *acc = p.acc + (int64_t)u * p.acc_stride;
   for (int i = rank * kPickThreads + tid; i < W; i += C * kPickThreads) kept[take + i] = n + i;
   if (take == 0) return;
-  if (n <= kPickThreads) {  // the same for the cluster
+  if (n <= kPickRank) {  // the same for the cluster
     if (rank != 0) return;
     const uint32_t key = tid < n ? sum_key(__ldg(acc + tid)) : 0u;
     sh_tot[tid] = key;
@@ -150,7 +151,8 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const EvictParams p)
     const uint4 *all = reinterpret_cast<const uint4 *>(sh_tot);
     const int mine = tid / 32 * 8, end = (n + 3) / 4;  // the warp's own keys
     int before = 0;
-    for (int j = 0; j < min(mine, end); ++j) {
+    if (mine < end) {  // not for the warps behind the last position
+    for (int j = 0; j < mine; ++j) {
       const uint4 x = all[j];
       before += (x.x >= key) + (x.y >= key) + (x.z >= key) + (x.w >= key);
     }
@@ -163,6 +165,7 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const EvictParams p)
     for (int j = mine + 8; j < end; ++j) {
       const uint4 x = all[j];
       before += (x.x > key) + (x.y > key) + (x.z > key) + (x.w > key);
+    }
     }
     const bool taken = tid < n && before < take;
     int tot;
@@ -231,18 +234,19 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const EvictParams p)
   // 16,384 each of a share whose keys are held; a longer share counts its totals first and walks its positions again.
   const int warp = tid >> 5, lane = tid & 31;
   const uint32_t below = (1u << lane) - 1u;
+  constexpr int kPickWarps = kPickThreads / 32;
   int tot_gt, tot_eq;
   if (held) {
 #pragma unroll
     for (int k = 0; k < kPickKeys; ++k) {
       const bool in = c0 + k * kPickThreads + tid < c1;
       const uint32_t mg = __ballot_sync(0xffffffffu, in && keys[k] > prefix), me = __ballot_sync(0xffffffffu, in && keys[k] == prefix);
-      if (lane == 0) sh_tot[k * 32 + warp] = (uint32_t)(__popc(mg) | (__popc(me) << 16));
+      if (lane == 0) sh_tot[k * kPickWarps + warp] = (uint32_t)(__popc(mg) | (__popc(me) << 16));
     }
     __syncthreads();
     int tot;
-    const int x = tid < kPickKeys * 32 ? (int)sh_tot[tid] : 0, before = block_exclusive_scan(x, sh_warp, &tot);
-    if (tid < kPickKeys * 32) sh_tot[tid] = (uint32_t)before;
+    const int x = tid < kPickKeys * kPickWarps ? (int)sh_tot[tid] : 0, before = block_exclusive_scan(x, sh_warp, &tot);
+    if (tid < kPickKeys * kPickWarps) sh_tot[tid] = (uint32_t)before;
     tot_gt = tot & 0xffff;
     tot_eq = tot >> 16;
   } else {
@@ -267,7 +271,7 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const EvictParams p)
     for (int k = 0; k < kPickKeys; ++k) {
       const int t = c0 + k * kPickThreads + tid;
       const bool is_gt = t < c1 && keys[k] > prefix, is_eq = t < c1 && keys[k] == prefix;
-      const uint32_t mg = __ballot_sync(0xffffffffu, is_gt), me = __ballot_sync(0xffffffffu, is_eq), before = sh_tot[k * 32 + warp];
+      const uint32_t mg = __ballot_sync(0xffffffffu, is_gt), me = __ballot_sync(0xffffffffu, is_eq), before = sh_tot[k * kPickWarps + warp];
       const int g = gt0 + (int)(before & 0xffffu) + __popc(mg & below), e = eq0 + (int)(before >> 16) + __popc(me & below);
       if (is_gt || (is_eq && e < need)) kept[g + min(e, need)] = t;
     }
@@ -318,10 +322,11 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const EvictParams p)
 // by the steps' latency, 1.2 us each.
 constexpr int kMoveThreads = 256;
 constexpr int kMoveRuns = 5;  // in the ring: one written, one awaited, three on the way
-constexpr int kMoveRows = 256;  // rows of a CTA's part of a run, at most
+constexpr int kMoveRows = 256;  // rows of a CTA's part of a run, at most (8 loads of 32 rows: a head has 128 bytes or more)
 
+template <int LOADS>
 struct MoveRing {
-  uint4 data[kMoveRuns][4 * kMoveThreads];
+  uint4 data[kMoveRuns][LOADS * kMoveThreads];
   int32_t from[2][kMoveRows];        // of the run that is copied next, and the one after it
   int32_t to[kMoveRuns][kMoveRows];  // -1: nothing moves
 };
@@ -333,9 +338,9 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const V *src) {
 }
 
 // LOADS elements per thread and run; `lanes` elements per row
-template <typename V, int LOADS>
+template <typename V, int LOADS, typename Ring>
 __device__ __forceinline__ void move_rows(uint8_t *base, int64_t row_bytes, int lanes, int col, const int32_t *kept, int K,
-                                          const EvictParams &p, int b, bool sums, MoveRing &ring) {
+                                          const EvictParams &p, int b, bool sums, Ring &ring) {
   cg::cluster_group cluster = cg::this_cluster();
   const int per = kMoveThreads / lanes, rows = per * LOADS, run = rows * (int)cluster.num_blocks();
   const int tid = threadIdx.x, r0 = tid / lanes, j_first = (int)cluster.block_rank() * rows;
@@ -432,9 +437,10 @@ __device__ __forceinline__ void move_rows(uint8_t *base, int64_t row_bytes, int 
   write(at == 0 ? kMoveRuns - 1 : at - 1);
   cp_async_wait_all();
 }
+template <int LOADS>
 __global__ void __launch_bounds__(kMoveThreads, 2) move_kernel(const EvictParams p) {
   extern __shared__ __align__(16) uint8_t move_smem[];
-  MoveRing &move_ring = *reinterpret_cast<MoveRing *>(move_smem);
+  MoveRing<LOADS> &move_ring = *reinterpret_cast<MoveRing<LOADS> *>(move_smem);
   griddep_wait();
   griddep_launch_dependents();
   const int u = blockIdx.x / (int)cg::this_cluster().num_blocks(), b = u / p.Hkv, kvh = u % p.Hkv, job = blockIdx.y;
@@ -444,7 +450,7 @@ __global__ void __launch_bounds__(kMoveThreads, 2) move_kernel(const EvictParams
   const int64_t row_bytes = (int64_t)p.Hkv * p.head_bytes;
   if (job < 2) {
     const int lanes = p.head_bytes / 16;
-    move_rows<uint4, 4>(static_cast<uint8_t *>(job == 0 ? p.k : p.v), row_bytes, lanes, kvh * p.head_bytes + (threadIdx.x % lanes) * 16,
+    move_rows<uint4, LOADS>(static_cast<uint8_t *>(job == 0 ? p.k : p.v), row_bytes, lanes, kvh * p.head_bytes + (threadIdx.x % lanes) * 16,
                      kept, p.budget, p, b, false, move_ring);
   } else if (job == 2) {
     move_rows<float, 1>(reinterpret_cast<uint8_t *>(p.acc + (int64_t)u * p.acc_stride), 4, 1, 0, kept, p.budget, p, b, true, move_ring);
@@ -468,15 +474,22 @@ cudaError_t launch_evict(const EvictParams &p0, bool scales, int sms, cudaStream
   int C = 1;  // shares of at least 2,048 positions, and no more CTAs than SMs
   while (C < 8 && p.t_cap > (int64_t)C * 4096 && (int64_t)units * C * 2 <= sms) C *= 2;
   cudaError_t e;
-  e = launch_ex(pick_kernel, dim3((unsigned)(units * C)), dim3(kPickThreads), 0, s, C, p);
+  // 16 positions per thread: two CTAs of 512 threads per SM for short sequences
+  e = p.t_cap <= 512 * kPickKeys ? launch_ex(pick_kernel<512>, dim3((unsigned)(units * C)), dim3(512), 0, s, C, p)
+                                 : launch_ex(pick_kernel<1024>, dim3((unsigned)(units * C)), dim3(1024), 0, s, C, p);
   if (e != cudaSuccess) return e;
   // CTAs per unit and job: no more than fit beside each other (two per SM), and a
   // run of theirs (at least 32 rows each) no longer than the budget
   C = 1;
   const int jobs = scales ? 5 : 3;
   while (C < 8 && (int64_t)units * 2 * C * 2 <= 2 * sms && p.budget > C * 64) C *= 2;
-  if ((e = set_smem_once(reinterpret_cast<const void *>(move_kernel), (int)sizeof(MoveRing))) != cudaSuccess) return e;
-  return launch_ex(move_kernel, dim3((unsigned)(units * C), jobs), dim3(kMoveThreads), (int)sizeof(MoveRing), s, C, p);
+  auto move = [&](auto kern, size_t bytes) {
+    const cudaError_t err = set_smem_once(reinterpret_cast<const void *>(kern), (int)bytes);
+    return err != cudaSuccess ? err : launch_ex(kern, dim3((unsigned)(units * C), jobs), dim3(kMoveThreads), bytes, s, C, p);
+  };
+  // Where one CTA per SM is enough, twice the rows per step: a step takes 1.2 us whatever it moves.
+  if ((int64_t)units * 2 * C <= sms) return move(move_kernel<8>, sizeof(MoveRing<8>));
+  return move(move_kernel<4>, sizeof(MoveRing<4>));
 }
 
 }  // namespace hs2

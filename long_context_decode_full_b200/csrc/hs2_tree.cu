@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) tree_combine_kernel(const 
   }
   __syncthreads();
   // a batch of records at a time, so that their loads are in flight together
-  constexpr int kBatch = 8;
+  constexpr int kBatch = 16;
   float M = -INFINITY, L = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
   for (int i0 = 0; i0 < records; i0 += kBatch) {
     float m[kBatch], l[kBatch];
