@@ -14,6 +14,7 @@
 // one wave of position chunks, plus the CTAs that join the records into the
 // attention output.
 #include "hs2_internal.h"
+#include "hs2_rows.cuh"
 #include "hs2_select_common.cuh"
 
 namespace hs2 {
@@ -110,38 +111,6 @@ __global__ void __launch_bounds__(kAccThreads) accumulate_kernel(const Accumulat
 // groups: 10 sequences of up to 17,430 tokens, 8 kv heads of one query head, d 128,
 // take 140 us with the update (525 us with that kernel; the bytes' floor is 111).
 constexpr int kRowWarps = 8, kRowTile = 64, kWarpRows = kRowTile / kRowWarps;
-
-template <int N>
-struct RowVec {
-  float x[N];
-  __device__ __forceinline__ void load(const float *p) {
-    if constexpr (N == 4) {
-      const float4 v = __ldg(reinterpret_cast<const float4 *>(p));
-      x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
-    } else {
-      const float2 v = __ldg(reinterpret_cast<const float2 *>(p));
-      x[0] = v.x, x[1] = v.y;
-    }
-  }
-};
-
-// Sums of N values over the 32 lanes: halves are exchanged while there are two or
-// more, so value i ends in the lanes whose upper log2 N bits are i (N <= 32), or in
-// the lane i / (N / 32), N / 32 values each.
-template <int N>
-__device__ __forceinline__ void sum_over_lanes(float *x, int lane) {
-  int o = 16;
-#pragma unroll
-  for (int n = N; n > 1 && o > 0; n >>= 1, o >>= 1) {
-    const bool up = lane & o;
-#pragma unroll
-    for (int i = 0; i < n / 2; ++i) {
-      const float give = up ? x[i] : x[i + n / 2], keep = up ? x[i + n / 2] : x[i];
-      x[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
-    }
-  }
-  for (; o > 0; o >>= 1) x[0] += __shfl_xor_sync(0xffffffffu, x[0], o);
-}
 
 template <int G, int D>
 __global__ void __launch_bounds__(32 * kRowWarps) rows_attn_f32_kernel(const FullParams p) {

@@ -44,8 +44,8 @@ TreePlan tree_plan(int B, int N, int Hkv, int G, int D, bool f32, int64_t t_cap)
   t.tile = tree_tc_tile();
   t.rows = tree_tc_rows();
   t.streams = f32 ? 1 : 2;
-  if (f32) {
-    t.rows = N * G <= 32 ? 32 : 64;
+  if (f32) {  // two blocks of few rows take 0.6 to 1.06 of the tiled kernel's time, three would take as long as it
+    t.rows = N * G <= 2 * tree_f32_few_rows() ? tree_f32_few_rows() : (N * G <= 32 ? 32 : 64);
     t.tile = t.rows == 32 && (t_cap + 63) / 64 * Hkv * B < sm_count() ? 32 : 64;
   }
   const int ctas = sm_count() * (f32 ? tree_f32_ctas_per_sm(D, t.rows, t.tile) : 1), per_block = t.rows * t.streams;

@@ -277,6 +277,7 @@ struct TreeParams {
   float *records;                    // [groups][kTreeSlots][blocks][streams] of rows * (D + 2)
 };
 int tree_f32_ctas_per_sm(int D, int rows, int keys);
+int tree_f32_few_rows();
 cudaError_t launch_tree_f32(const TreeParams &p, cudaStream_t s);
 int tree_tc_rows();
 int tree_tc_tile();

@@ -9,7 +9,8 @@
 // the operands): a CTA of 16 x 16 threads takes 64 rows x 64 positions, each
 // thread a 4 x 4 block of the logits and 4 rows x D / 16 columns of the output
 // in registers (half the rows where a unit has at most 32, and half the positions
-// where the tiles would not fill the GPU); Q, K, V and the weights are in shared memory, K's and Q's rows
+// where the tiles would not fill the GPU; at most 16 rows have a kernel of their own,
+// below); Q, K, V and the weights are in shared memory, K's and Q's rows
 // padded by 16 bytes so that 16-byte reads of 8 rows meet 32 banks.  Bound by the
 // FMA units on long caches, by latency on short ones: 5 drafts x 4 heads over 2,048
 // tokens take 14.8 us with the joining kernel (64-row, 64-position shapes and shares
@@ -18,6 +19,7 @@
 
 #include "hs2.h"
 #include "hs2_internal.h"
+#include "hs2_rows.cuh"
 #include "hs2_tree_common.cuh"
 
 namespace hs2 {
@@ -216,6 +218,188 @@ __global__ void __launch_bounds__(kThreads) tree_f32_kernel(const TreeParams p) 
   }
 }
 
+// ------------------------------------------------------------------ few rows
+// fp32 caches and at most 16 query rows of a unit, in blocks of 8: too little work
+// per byte for tiles that pass through shared memory.  A warp takes 8 positions of
+// every tile for all 8 rows, its lanes D / 32 dimensions each, and K, V, Q and the
+// output stay in registers; while it works on four positions the next four are on
+// their way.  The products' partial sums are added by halving exchanges, which leave
+// lane 8 j + r with the logit of row r at position j; the weights return through shared
+// memory, and the warps' sums are joined at a segment's end.
+//   1 draft x 8 heads over 60,000 tokens, 4 KV heads, D 128: 78.5 us (the tiled kernel 213)
+//   2 x 8 of the same: 135 us (213); 4 x 4, 2,500 tokens, 8 KV heads: 22.4 us (36.0)
+//   D 64, 8 sequences of 20,000, 4 x 4: 266 us (290); 4 of 979: 16.9 us (15.9)
+// 8 rows over 27 x 10,575 tokens take 313 us (3.7 TB/s), 16 rows 594 us (882): each block
+// reads K and V, so three blocks would take what the tiled kernel does.  Bound by the
+// issue of two warps per scheduler (0.48 instructions a cycle, a quarter of the waiting
+// for loads): 566 instructions per four positions, 256 of them products.
+constexpr int kFewRows = 8, kFewWarps = 8, kFewKeys = 64, kWarpKeys = kFewKeys / kFewWarps, kStepKeys = 4;
+
+template <int D>
+__global__ void __launch_bounds__(32 * kFewWarps, 1) tree_f32_few_kernel(const TreeParams p) {
+  extern __shared__ int32_t few_prefix[];
+  constexpr int R = kFewRows, NV = D / 32, NS = kStepKeys * R;
+  static_assert(NS == 32 && kWarpKeys == 2 * kStepKeys, "a sum per lane, two steps a tile");
+  __shared__ __align__(16) float sh_s[kFewWarps][NS];
+  __shared__ float sh_m[kFewWarps][R], sh_l[kFewWarps][R], sh_o[kFewWarps][R * D];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int block = blockIdx.x % p.blocks;
+  const int64_t group = blockIdx.x / p.blocks;
+  griddep_wait();
+  griddep_launch_dependents();
+  if (warp == 0) tree_prefix(p, few_prefix);
+  __syncthreads();
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i <= p.B; i += 32 * kFewWarps) p.prefix[i] = few_prefix[i];
+  const int64_t total = (int64_t)p.Hkv * few_prefix[p.B];
+  if (total == 0) return;
+  const TreeShare share(total, p.groups);
+  const int64_t g0 = share.start(group), g1 = share.start(group + 1);
+  for (int64_t g = g0; g < g1;) {
+    const int b = tree_seq(few_prefix, p.B, p.Hkv, g), nb = few_prefix[b + 1] - few_prefix[b];
+    const int64_t at0 = g - (int64_t)p.Hkv * few_prefix[b];
+    const int kvh = (int)(at0 / nb), i0 = (int)(at0 % nb), i1 = (int)min((int64_t)nb, i0 + (g1 - g));
+    const bool begins = g == g0;
+    g += i1 - i0;
+    const int T = tree_len(p, b), n = tree_drafts(p, b, T), first = T - n;
+    const int row0 = block * R, nrows = min(R, n * p.G - row0);
+    if (nrows <= 0) continue;  // the same for the whole CTA
+    RowVec<NV> q[R];
+    float m = -INFINITY, l = 0.f, o[R][NV];  // m of row lane % R; l over this lane's positions alone
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int row = row0 + min(r, nrows - 1), h = kvh * p.G + row % p.G;
+      q[r].load(static_cast<const float *>(p.q) + ((int64_t)b * p.N + row / p.G) * p.q_stride + (int64_t)h * D + lane * NV);
+#pragma unroll
+      for (int e = 0; e < NV; ++e) o[r][e] = 0.f;
+    }
+    // the slots of a warp's positions in tile i, one per lane
+    auto look = [&](int i) -> int64_t {
+      const int t = i * kFewKeys + warp * kWarpKeys + lane % kWarpKeys;
+      return i < i1 && t < T ? tree_slot(p, b, t) : -1;
+    };
+    auto fetch = [&](RowVec<NV> *k, RowVec<NV> *v, int64_t mine, int half) {
+      const int64_t row = (max(mine, (int64_t)0) * p.Hkv + kvh) * D;
+#pragma unroll
+      for (int j = 0; j < kStepKeys; ++j) {
+        const int64_t at = __shfl_sync(0xffffffffu, row, half * kStepKeys + j) + lane * NV;
+        k[j].load(static_cast<const float *>(p.k) + at);
+        v[j].load(static_cast<const float *>(p.v) + at);
+      }
+    };
+    auto step = [&](RowVec<NV> *k, RowVec<NV> *v, int64_t mine, int half, int t0) {
+      if (__any_sync(0xffffffffu, mine < 0)) {  // no position, or no such page: zeros
+#pragma unroll
+        for (int j = 0; j < kStepKeys; ++j) {
+          if (__shfl_sync(0xffffffffu, mine, half * kStepKeys + j) < 0) {
+#pragma unroll
+            for (int e = 0; e < NV; ++e) k[j].x[e] = v[j].x[e] = 0.f;
+          }
+        }
+      }
+      float s[NS];
+#pragma unroll
+      for (int j = 0; j < kStepKeys; ++j)
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          float a = 0.f;
+#pragma unroll
+          for (int e = 0; e < NV; ++e) a = fmaf(q[r].x[e], k[j].x[e], a);
+          s[j * R + r] = a;
+        }
+      sum_over_lanes<NS>(s, lane);
+      const bool plain = t0 + kStepKeys <= first;  // positions of the context alone: all are seen
+      float x = s[0] * p.c2;                       // of row lane % R at position t0 + lane / R
+      if (!plain) {
+        const int t = t0 + lane / R, r = lane % R;
+        if (t >= first) x = t < T && r < nrows && ((tree_bits(p, b, (row0 + r) / p.G, n) >> (t - first)) & 1ull) ? x : -INFINITY;
+      }
+      float top = fmaxf(m, x);
+#pragma unroll
+      for (int d = R; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      const float at = top == -INFINITY ? 0.f : top, alpha = m == top ? 1.f : exp2f(m - at), w = exp2f(x - at);
+      m = top;
+      l = fmaf(l, alpha, w);
+      sh_s[warp][lane] = w;
+      if (__any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const float f = __shfl_sync(0xffffffffu, alpha, r);
+#pragma unroll
+          for (int e = 0; e < NV; ++e) o[r][e] *= f;
+        }
+      }
+      __syncwarp();
+#pragma unroll
+      for (int e = 0; e < NS; e += 4) {
+        const float4 y = *reinterpret_cast<const float4 *>(&sh_s[warp][e]);
+        s[e] = y.x, s[e + 1] = y.y, s[e + 2] = y.z, s[e + 3] = y.w;
+      }
+      __syncwarp();
+      // in the draft, a value that a row does not see must not reach it, not even as 0 * NaN
+      if (plain) {
+#pragma unroll
+        for (int j = 0; j < kStepKeys; ++j)
+#pragma unroll
+          for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int e = 0; e < NV; ++e) o[r][e] = fmaf(s[j * R + r], v[j].x[e], o[r][e]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kStepKeys; ++j)
+#pragma unroll
+          for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int e = 0; e < NV; ++e) o[r][e] = s[j * R + r] == 0.f ? o[r][e] : fmaf(s[j * R + r], v[j].x[e], o[r][e]);
+      }
+    };
+    // while four positions are worked on, the next four are on their way
+    RowVec<NV> k0[kStepKeys], v0[kStepKeys], k1[kStepKeys], v1[kStepKeys];
+    int64_t mine = look(i0), next = look(i0 + 1);
+    fetch(k0, v0, mine, 0);
+    for (int i = i0; i < i1; ++i) {
+      const int t0 = i * kFewKeys + warp * kWarpKeys;
+      fetch(k1, v1, mine, 1);
+      step(k0, v0, mine, 0, t0);
+      fetch(k0, v0, next, 0);
+      step(k1, v1, mine, 1, t0 + kStepKeys);
+      mine = next, next = look(i + 2);
+    }
+#pragma unroll
+    for (int d = R; d < 32; d <<= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+    if (lane < R) sh_m[warp][lane] = m, sh_l[warp][lane] = l;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int e = 0; e < NV; ++e) sh_o[warp][r * D + lane * NV + e] = o[r][e];
+    __syncthreads();
+    const bool whole = i0 == 0 && i1 == nb;
+    float *rec = tree_record(p, group, begins ? 0 : 1, block, 0);
+    for (int e = threadIdx.x; e < nrows * D; e += 32 * kFewWarps) {
+      const int r = e / D, dim = e % D;
+      float M = -INFINITY, L = 0.f, O = 0.f;
+#pragma unroll
+      for (int w = 0; w < kFewWarps; ++w) M = fmaxf(M, sh_m[w][r]);
+      const float at = M == -INFINITY ? 0.f : M;
+#pragma unroll
+      for (int w = 0; w < kFewWarps; ++w) {
+        const float f = exp2f(sh_m[w][r] - at);
+        L = fmaf(f, sh_l[w][r], L);
+        O = fmaf(f, sh_o[w][e], O);
+      }
+      if (whole) {
+        const float inv = L > 0.f || L != L ? 1.f / L : 0.f;  // nothing seen: zeros
+        const int row = row0 + r, h = kvh * p.G + row % p.G;
+        static_cast<float *>(p.out)[((int64_t)b * p.N + row / p.G) * p.out_stride + (int64_t)h * D + dim] = O * inv;
+      } else {
+        if (dim == 0) rec[r] = M, rec[R + r] = L;
+        rec[2 * R + ((dim / 4) * R + r) * 4 + dim % 4] = O;
+      }
+    }
+    __syncthreads();  // shared memory is free for the next segment
+  }
+}
+
 // ------------------------------------------------------------------ combine
 // out = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s over the records s of a
 // cut unit, in the order of its shares.
@@ -236,11 +420,12 @@ __global__ void __launch_bounds__(32 * kCombineWarps) tree_combine_kernel(const 
   const TreeShare share(total, p.groups);
   const int64_t U0 = (int64_t)p.Hkv * before + (int64_t)kvh * nb;
   const int64_t c0 = share.owner(U0), c1 = share.owner(U0 + nb - 1);
-  // 32 rows lie in one block, and in one stream's rows
+  // 32 rows lie in one block and in one stream's rows, or in several blocks of fewer rows
   const int per_block = p.rows * p.streams, block = row0 / per_block, in_block = row0 % per_block;
   const bool dealt = min(per_block, n * p.G - block * per_block) > p.rows;  // the streams have rows of their own
   const int streams = dealt ? 1 : p.streams, s0 = dealt ? in_block / p.rows : 0;
-  const int r = (dealt ? in_block % p.rows : in_block) + lane;
+  const int row_here = min(row0 + lane, n * p.G - 1), r = row_here % (dealt ? p.rows : per_block);
+  const int64_t shift = (int64_t)(row_here / per_block - block) * p.streams * p.rows * (p.D + 2);
   if (c0 == c1) return;  // finished by its CTA
   const int records = (int)(c1 - c0 + 1) * streams;
   for (int i = threadIdx.x; i < records; i += 32 * kCombineWarps) {
@@ -260,7 +445,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) tree_combine_kernel(const 
       const int64_t x = i0 + k < records ? sh_at[i0 + k] : -1;
       m[k] = -INFINITY, l[k] = 0.f, v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (x >= 0) {
-        const float *rec = p.records + x;
+        const float *rec = p.records + x + shift;
         m[k] = __ldcg(rec + r);
         l[k] = __ldcg(rec + p.rows + r);
         v[k] = __ldcg(reinterpret_cast<const float4 *>(rec + 2 * p.rows) + (size_t)col4 * p.rows + r);
@@ -294,7 +479,9 @@ __global__ void __launch_bounds__(32 * kCombineWarps) tree_combine_kernel(const 
 
 }  // namespace
 
+int tree_f32_few_rows() { return kFewRows; }
 int tree_f32_ctas_per_sm(int D, int rows, int keys) {
+  if (rows == kFewRows) return 1;
   if (D == 64) return rows == 32 && keys == 32 ? 3 : 2;
   return rows == 32 ? 2 : 1;
 }
@@ -312,6 +499,13 @@ cudaError_t launch_tree_f32(const TreeParams &p, cudaStream_t s) {
   };
   using S32 = std::integral_constant<int, 32>;
   using S64 = std::integral_constant<int, 64>;
+  if (p.rows == kFewRows) {
+    auto few = [&](auto kern) {
+      const cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kern), (kMaxBatchSmem + 1) * 4);
+      return e != cudaSuccess ? e : launch_ex(kern, dim3((unsigned)(p.groups * p.blocks)), dim3(32 * kFewWarps), (size_t)(p.B + 1) * 4, s, 0, p);
+    };
+    return p.D == 64 ? few(tree_f32_few_kernel<64>) : few(tree_f32_few_kernel<128>);
+  }
   if (p.rows == 32) return p.tile == 32 ? shape(S32{}, S32{}) : shape(S32{}, S64{});
   return shape(S64{}, S64{});
 }

@@ -76,9 +76,9 @@ __device__ __forceinline__ int tree_seq(const int32_t *prefix, int B, int Hkv, i
   return lo;
 }
 __device__ __forceinline__ int64_t tree_slot(const TreeParams &p, int b, int64_t pos) {
+  const uint32_t at = (uint32_t)pos, ps = (uint32_t)p.page_size;  // lengths fit 31 bits
   const int64_t s = p.page_table == nullptr ? (int64_t)b * p.page_size + pos
-                                            : (int64_t)__ldg(p.page_table + (int64_t)b * p.max_pages + pos / p.page_size) *
-                                                      p.page_size + pos % p.page_size;
+                                            : (int64_t)__ldg(p.page_table + (int64_t)b * p.max_pages + at / ps) * ps + at % ps;
   return s >= 0 && s < p.num_slots ? s : -1;
 }
 __device__ __forceinline__ size_t tree_record_at(const TreeParams &p, int64_t group, int slot, int block, int stream) {

@@ -63,6 +63,10 @@ TREES = [
     ("f32", 1, 4, 64, 0, 5, [2048, 5, 6], [5, 5, 0]),
     ("f32", 2, 8, 128, 48, 33, [100, 33, 511], [33, 33, 20]),
     ("f32", 2, 1, 64, 16, 64, [64, 1, 700], [64, 1, 64]),
+    ("f32", 2, 4, 128, 64, 4, [3000, 4, 0, 65], [4, 4, 1, 3]),
+    ("f32", 3, 1, 64, 16, 16, [129, 16, 20000], [16, 9, 16]),
+    ("f32", 1, 8, 128, 0, 1, [5000, 1], [1, 1]),
+    ("f32", 1, 4, 128, 128, 8, [900, 31], [8, 5]),
 ]
 
 
