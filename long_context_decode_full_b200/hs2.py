@@ -7,6 +7,7 @@ there is no fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import NamedTuple, Optional, Sequence
@@ -180,6 +181,16 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(s.cuda_stream)
 
 
+_CURRENT = contextlib.nullcontext()
+
+
+def _on(stream):
+    """Where a call makes the results and workspaces that it is not given: on the stream that it runs on, so that their
+    fills come before its kernels and their memory is used again only behind them.  As with tensors made under
+    torch.cuda.stream(), a result used on another stream is ordered by the caller."""
+    return _CURRENT if stream is None else torch.cuda.stream(stream)
+
+
 def cache_desc(kv: torch.Tensor, scale: Optional[torch.Tensor], page_size: int) -> Cache:
     assert kv.dim() == 3 and kv.is_contiguous(), "cache must be a contiguous [num_slots, Hkv, d] tensor"
     return Cache(kv.data_ptr(), None if scale is None else scale.data_ptr(), _DTYPE[kv.dtype], kv.shape[1],
@@ -221,12 +232,13 @@ def full_attn_select(q, k, v, seq_lens, page_table=None, page_size=None, window=
         page_size = k.shape[0] // B
     max_pages = 1 if page_table is None else page_table.shape[1]
     t_cap = page_size * max_pages
-    if out is None:
-        out = torch.empty_like(q)
-    if idx_out is None:
-        idx_out = torch.empty(B, Hkv, window + k_global, dtype=torch.int32, device=q.device)
-    if workspace is None:
-        workspace = alloc_workspace(B, Hkv, Hq // Hkv, d, t_cap, q.device)
+    with _on(stream):
+        if out is None:
+            out = torch.empty_like(q)
+        if idx_out is None:
+            idx_out = torch.empty(B, Hkv, window + k_global, dtype=torch.int32, device=q.device)
+        if workspace is None:
+            workspace = alloc_workspace(B, Hkv, Hq // Hkv, d, t_cap, q.device)
     kc, vc = cache_desc(k, k_scale, page_size), cache_desc(v, v_scale, page_size)
     qd, od = heads_desc(q), heads_desc(out)
     if fused:
@@ -260,12 +272,13 @@ def full_attn_select_blocks(q, k, v, seq_lens, page_table=None, page_size=None, 
         assert page_table is None, "page_size is required with a page table"
         page_size = k.shape[0] // B
     max_pages = 1 if page_table is None else page_table.shape[1]
-    if out is None:
-        out = torch.empty_like(q)
-    if idx_out is None:
-        idx_out = torch.empty(B, Hkv, window + k_global, dtype=torch.int32, device=q.device)
-    if workspace is None:
-        workspace = alloc_workspace(B, Hkv, Hq // Hkv, d, page_size * max_pages, q.device)
+    with _on(stream):
+        if out is None:
+            out = torch.empty_like(q)
+        if idx_out is None:
+            idx_out = torch.empty(B, Hkv, window + k_global, dtype=torch.int32, device=q.device)
+        if workspace is None:
+            workspace = alloc_workspace(B, Hkv, Hq // Hkv, d, page_size * max_pages, q.device)
     kc, vc = cache_desc(k, k_scale, page_size), cache_desc(v, v_scale, page_size)
     qd, od = heads_desc(q), heads_desc(out)
     _check(lib().hs2_full_attn_select_blocks(ctypes.byref(qd), ctypes.byref(kc), ctypes.byref(vc), _ptr(seq_lens),
@@ -289,10 +302,11 @@ def full_attn_select_static(q, k, v, seq_lens, page_table=None, page_size=None, 
         assert page_table is None, "page_size is required with a page table"
         page_size = k.shape[0] // B
     max_pages = 1 if page_table is None else page_table.shape[1]
-    if out is None:
-        out = torch.empty_like(q)
-    if idx_out is None:
-        idx_out = torch.empty(B, Hkv, window + k_global, dtype=torch.int32, device=q.device)
+    with _on(stream):
+        if out is None:
+            out = torch.empty_like(q)
+        if idx_out is None:
+            idx_out = torch.empty(B, Hkv, window + k_global, dtype=torch.int32, device=q.device)
     kc, vc = cache_desc(k, k_scale, page_size), cache_desc(v, v_scale, page_size)
     qd, od = heads_desc(q), heads_desc(out)
     _check(lib().hs2_full_attn_select_static(ctypes.byref(qd), ctypes.byref(kc), ctypes.byref(vc),
@@ -312,7 +326,8 @@ def sparse_attn(q_l, k, v, idx, k_scale=None, v_scale=None, page_size=1, out=Non
     _need("idx", idx, torch.int32, dim=3)
     _need_cuda(q=q_l, k=k, v=v, idx=idx)
     if out is None:
-        out = torch.empty_like(q_l)
+        with _on(stream):
+            out = torch.empty_like(q_l)
     kc, vc = cache_desc(k, k_scale, page_size), cache_desc(v, v_scale, page_size)
     qd, od = heads_desc(q_l), heads_desc(out)
     _check(lib().hs2_sparse_attn(ctypes.byref(qd), ctypes.byref(kc), ctypes.byref(vc), _ptr(idx), idx.shape[-1],
@@ -372,7 +387,8 @@ def kv_bridge_append(hidden, w_k, w_v, k, v, seq_lens, page_table=None, page_siz
         n = kv_bridge_workspace_bytes(B, dm, k.shape[1], k.shape[2])
         if n == 0:
             raise HS2Error(ERR_INVALID_ARG, "invalid KV bridge shape")
-        workspace = torch.zeros(n, dtype=torch.uint8, device=hidden.device)
+        with _on(stream):
+            workspace = torch.zeros(n, dtype=torch.uint8, device=hidden.device)
     kc, vc = cache_desc(k, k_scale, page_size), cache_desc(v, v_scale, page_size)
     _check(lib().hs2_kv_bridge_append(_ptr(hidden), B, dm, _ptr(w_k), _ptr(w_v), _ptr(seq_lens), _ptr(page_table),
                                       max_pages, ctypes.byref(kc), ctypes.byref(vc), _ptr(workspace),
@@ -502,7 +518,8 @@ def rope_append(q, k_new, v_new, positions, table: RopeTable, k, v, seq_lens, pa
     if q is not None:
         qt = _tokens("q", q, _q_dtype(k))
         if q_out is None:
-            q_out = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
+            with _on(stream):
+                q_out = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
         _arg("q_out", q_out, q.dtype, q.shape)
     pp, lp = _arg("positions", positions, torch.int32, (B, N)), _arg("seq_lens", seq_lens, torch.int32, (B,))
     np_ = _arg("num_new", num_new, torch.int32, (B,))
@@ -552,14 +569,16 @@ def tree_attn(q, k, v, seq_lens, page_table=None, page_size=None, tree_mask=None
     qt = _tokens("q", q, _q_dtype(k))
     B, N = qt.batch, qt.tokens
     if out is None:
-        out = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
+        with _on(stream):
+            out = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
     ot = _tokens("out", out, q.dtype)
     mp, lp = _arg("tree_mask", tree_mask, torch.int64, (B, N)), _arg("seq_lens", seq_lens, torch.int32, (B,))
     np_ = _arg("num_draft", num_draft, torch.int32, (B,))
     kc, vc, pages, max_pages = _paged(k, v, k_scale, v_scale, page_table, page_size, B)
     device = _device(_TREE_NAMES, k, v, q, out, tree_mask, seq_lens, num_draft, page_table, k_scale, v_scale, workspace)
     if workspace is None:
-        workspace = alloc_tree_workspace(q, k)
+        with _on(stream):
+            workspace = alloc_tree_workspace(q, k)
     _need("workspace", workspace, torch.uint8)
     _run(lib().hs2_tree_attn, device, stream, qt, kc, vc, lp, np_, mp, pages, max_pages, ot, workspace.data_ptr(),
          workspace.numel())
@@ -578,7 +597,8 @@ def tree_accept(k, v, seq_lens, path, path_len, page_table=None, page_size=None,
     np_ = _arg("num_draft", num_draft, torch.int32, one)
     kc, vc, pages, max_pages = _paged(k, v, k_scale, v_scale, page_table, page_size, B)
     if lens_out is None:
-        lens_out = torch.empty_like(seq_lens)
+        with _on(stream):
+            lens_out = torch.empty_like(seq_lens)
     op = _arg("lens_out", lens_out, torch.int32, one)
     device = _device(_ACCEPT_NAMES, k, v, seq_lens, path, path_len, num_draft, page_table, k_scale, v_scale, lens_out)
     _run((_lib or lib()).hs2_tree_accept, device, stream, kc, vc, lp, np_, pp, ap, B, M, pages, max_pages, op)
@@ -603,11 +623,12 @@ def full_attn_accumulate(q, k, v, seq_lens, acc, page_table=None, page_size=None
     kc, vc, pages, max_pages = _paged(k, v, k_scale, v_scale, page_table, page_size, B)
     cap, sums = _sums(acc, B, k.shape[1])
     if out is None:
-        out = torch.empty_like(q)
+        with _on(stream):
+            out = torch.empty_like(q)
     _arg("out", out, q.dtype, q.shape)
     device = _device(_ACCUMULATE_NAMES, k, v, q, seq_lens, acc, page_table, k_scale, v_scale, out, workspace)
     if workspace is None:
-        with torch.cuda.device(device):
+        with torch.cuda.device(device), _on(stream):
             workspace = alloc_workspace(B, k.shape[1], Hq // k.shape[1], d, kc.page_size * max_pages, k.device)
     _need("workspace", workspace, torch.uint8)
     _run(lib().hs2_full_attn_accumulate, device, stream, heads_desc(q), kc, vc, lp, pages, max_pages, decay, fresh, sums,
@@ -625,10 +646,11 @@ def cache_evict(k, v, seq_lens, acc, budget, window=128, page_table=None, page_s
     kc, vc, pages, max_pages = _paged(k, v, k_scale, v_scale, page_table, page_size, B)
     Hkv = k.shape[1]
     cap, sums = _sums(acc, B, Hkv)
-    if kept is None:
-        kept = torch.empty(B, Hkv, max(budget, 0), dtype=torch.int32, device=k.device)
-    if lens_out is None:
-        lens_out = torch.empty_like(seq_lens)
+    with _on(stream):
+        if kept is None:
+            kept = torch.empty(B, Hkv, max(budget, 0), dtype=torch.int32, device=k.device)
+        if lens_out is None:
+            lens_out = torch.empty_like(seq_lens)
     kp, op = _arg("kept", kept, torch.int32, (B, Hkv, budget)), _arg("lens_out", lens_out, torch.int32, (B,))
     device = _device(_EVICT_NAMES, k, v, seq_lens, acc, page_table, k_scale, v_scale, kept, lens_out)
     _run(lib().hs2_cache_evict, device, stream, kc, vc, lp, B, pages, max_pages, sums, cap, budget, window, kp, op)

@@ -1,0 +1,83 @@
+"""What the drafted-token and bounded-cache calls promise beside their formulas: where results and workspaces are made,
+counts of each sequence's own, paths narrower than the draft, codes that both appends write, rows and sums that nothing
+may read.  Plain 64-bit forms in tests/draft_ref.py."""
+import pytest
+import torch
+
+import draft_ref as R
+from test_gpu_draft import gen, i32
+from long_context_decode_full_b200 import hs2
+
+pytestmark = pytest.mark.gpu
+BUSY = 100_000_000  # cycles, some 50 ms: longer than any call here
+
+
+# ---------------------------------------------------------------- another stream
+class StreamCase:
+    """One cache and the arguments of every call on it; a call takes a stream and leaves out all that is optional."""
+
+    def __init__(self):
+        hkv, G, d, N, B = 2, 4, 128, 5, 2
+        self.c = c = R.PagedCache("bf16", [700, 90], hkv, d, 16, seed=41, poison=False)
+        qkv = torch.randn(B, N, hkv * (G + 2), d, device="cuda", generator=gen(42)).bfloat16()
+        pos = torch.randint(0, 900, (B, N), device="cuda", generator=gen(43), dtype=torch.int32)
+        table, q = hs2.rope_table(128), qkv[:, :, :hkv * G]
+        kn, vn = qkv[:, :, hkv * G:hkv * (G + 1)], qkv[:, :, hkv * (G + 1):]
+        self.acc = acc = torch.rand(B, hkv, c.cap, device="cuda", generator=gen(44))
+        path, plen = i32([[1, 3, 4, 0, 0], [0, 2, 4, 0, 0]]), i32([3, 2])
+        hidden = torch.randn(B, 256, device="cuda", generator=gen(45)).bfloat16()
+        w = torch.randn(256, hkv * d, device="cuda", generator=gen(46)).bfloat16()
+        q1 = q[:, 0].contiguous()
+        idx = c.slots(0, torch.arange(40)).to(torch.int32).expand(B, hkv, 40).contiguous()
+        pg = dict(page_table=c.table, page_size=c.page)
+        self.calls = {
+            "rope_append": lambda s: hs2.rope_append(q, kn, vn, pos, table, c.k, c.v, c.lens, stream=s, **pg),
+            "tree_attn": lambda s: hs2.tree_attn(q, c.k, c.v, c.lens, stream=s, **pg),
+            "tree_accept": lambda s: hs2.tree_accept(c.k, c.v, c.lens, path, plen, stream=s, **pg),
+            "full_attn_accumulate": lambda s: hs2.full_attn_accumulate(q1, c.k, c.v, c.lens, acc, stream=s, **pg),
+            "cache_evict": lambda s: hs2.cache_evict(c.k, c.v, c.lens, acc, 80, 10, stream=s, **pg),
+            "kv_bridge_append": lambda s: hs2.kv_bridge_append(hidden, w, w, c.k, c.v, c.lens, stream=s, **pg),
+            "full_attn_select": lambda s: hs2.full_attn_select(q1, c.k, c.v, c.lens, window=16, k_global=32, stream=s, **pg),
+            "full_attn_select_blocks": lambda s: hs2.full_attn_select_blocks(q1, c.k, c.v, c.lens, window=16, k_global=32,
+                                                                             stream=s, **pg),
+            "full_attn_select_static": lambda s: hs2.full_attn_select_static(q1, c.k, c.v, c.lens, window=16, k_global=32,
+                                                                             stream=s, **pg),
+            "sparse_attn": lambda s: hs2.sparse_attn(q1, c.k, c.v, idx, stream=s),
+        }
+        self.state = [c.k, c.v, acc]
+        self.start = [x.clone() for x in self.state]
+
+    def reset(self):
+        for x, y in zip(self.state, self.start):
+            x.copy_(y)
+
+
+def results(r):
+    return [] if r is None else [r] if torch.is_tensor(r) else list(r)
+
+
+STREAM_CALLS = ["rope_append", "tree_attn", "tree_accept", "full_attn_accumulate", "cache_evict", "kv_bridge_append",
+                "full_attn_select", "full_attn_select_blocks", "full_attn_select_static", "sparse_attn"]
+
+
+@pytest.mark.parametrize("busy", ["current", "given"])
+@pytest.mark.parametrize("name", STREAM_CALLS)
+def test_results_and_workspaces_belong_to_the_given_stream(name, busy):
+    """A call on another stream makes what it is not given on that stream: nothing queued on the current one may reach
+    its results, and no memory of the call may pass to the current stream while the call runs."""
+    case = StreamCase()
+    want = [x.clone() for x in results(case.calls[name](None)) + case.state]
+    case.reset()
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    if busy == "current":  # a fill of a result on the current stream would come after the call
+        torch.cuda._sleep(BUSY)
+        got = results(case.calls[name](s))
+    else:  # the call waits; memory that it gave back would be taken and overwritten meanwhile
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(BUSY)
+        got = results(case.calls[name](s))
+        taken = [torch.full((n,), 0xA5, dtype=torch.uint8, device="cuda") for n in [1 << 8, 1 << 12, 1 << 16, 1 << 20] * 20 + [1 << 26] * 4]
+    torch.cuda.synchronize()
+    for x, y in zip(got + case.state, want):
+        assert torch.equal(R.bits(x), R.bits(y))
