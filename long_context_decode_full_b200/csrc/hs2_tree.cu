@@ -416,10 +416,12 @@ __global__ void __launch_bounds__(32 * kCombineWarps) tree_combine_kernel(const 
   const int row0 = blockIdx.x / (D / 32) * 32, col4 = blockIdx.x % (D / 32) * kCombineWarps + (threadIdx.x >> 5);
   const int T = tree_len(p, b), n = tree_drafts(p, b, T), before = p.prefix[b], nb = p.prefix[b + 1] - before;
   const int64_t total = (int64_t)p.Hkv * p.prefix[p.B];  // all fetched together
-  if (row0 >= n * p.G || nb == 0) return;
+  // Two calls that use one workspace at once (which the caller has to rule out) leave another call's tiles here: the
+  // outputs are theirs to lose, but every place that follows from the tiles has to lie in this workspace's records.
+  if (row0 >= n * p.G || nb <= 0 || before < 0 || total <= 0) return;
   const TreeShare share(total, p.groups);
   const int64_t U0 = (int64_t)p.Hkv * before + (int64_t)kvh * nb;
-  const int64_t c0 = share.owner(U0), c1 = share.owner(U0 + nb - 1);
+  const int64_t last = share.groups - 1, c0 = min(share.owner(U0), last), c1 = min(share.owner(U0 + nb - 1), last);
   // 32 rows lie in one block and in one stream's rows, or in several blocks of fewer rows
   const int per_block = p.rows * p.streams, block = row0 / per_block, in_block = row0 % per_block;
   const bool dealt = min(per_block, n * p.G - block * per_block) > p.rows;  // the streams have rows of their own

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import draft_ref as R
-from test_gpu_draft import gen, i32
+from test_gpu_draft import check, gen, i32, tree_case
 from long_context_decode_full_b200 import hs2
 
 pytestmark = pytest.mark.gpu
@@ -81,3 +81,41 @@ def test_results_and_workspaces_belong_to_the_given_stream(name, busy):
     torch.cuda.synchronize()
     for x, y in zip(got + case.state, want):
         assert torch.equal(R.bits(x), R.bits(y))
+
+
+# ---------------------------------------------------------------- a workspace used twice at once
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3", "f32"])
+def test_tree_attn_graphs_that_share_a_workspace(dtype):
+    """One workspace for two captured calls of other lengths and batches: right one after the other.  At once their
+    outputs are undefined, but nothing outside the workspace is touched, and a call after them is right."""
+    sides = [tree_case(dtype, 2, 4, 128, 64, 9, lens, [9] * len(lens), seed=s)
+             for s, lens in ((1, [3000, 400]), (2, [9, 70, 20000, 11, 12, 500, 64, 65]))]
+    refs = [R.tree_reference(c, q, [9] * len(c.T), masks, dtype) for c, q, masks, _ in sides]
+    ws = max((hs2.alloc_tree_workspace(q, c.k) for c, q, _, _ in sides), key=lambda w: w.numel())
+    ws = torch.cat([ws, torch.full((1 << 16,), 0x5A, dtype=torch.uint8, device="cuda")])  # the end is not the calls'
+    n, graphs, outs, streams = ws.numel() - (1 << 16), [], [], [torch.cuda.Stream() for _ in sides]
+    for c, q, _, words in sides:
+        out = torch.full_like(q, 77.0)
+        call = lambda: hs2.tree_attn(q, c.k, c.v, c.lens, tree_mask=words, out=out, workspace=ws[:n], **c.kw())  # noqa: B023, E731
+        call()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call()
+        graphs.append(g)
+        outs.append(out)
+    def each():
+        for g, out, (want, bound) in zip(graphs, outs, refs):
+            out.fill_(77.0)
+            g.replay()
+            torch.cuda.synchronize()
+            check(out, want, bound, ~want.isnan())
+    each()
+    for _ in range(50):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    assert hs2.workspace_status(ws[:n]) == hs2.OK
+    each()
+    assert bool((ws[n:] == 0x5A).all())
