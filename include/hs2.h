@@ -374,7 +374,11 @@ int hs2_tree_accept(const hs2_cache *k_cache, const hs2_cache *v_cache, const in
  *                                                  the softmax probability at t;
  * the newest `fresh` positions start with w_t (their old contents are not read),
  * so the sums need no initialisation while a cache grows by `fresh` tokens a step.
- * Positions t >= T_b are not touched.
+ * `fresh` has to be the number of positions that the sequence gained since the last
+ * call: a smaller one reads sums that nothing has set, a larger one drops earned ones.
+ * Where sequences gain different numbers (accepted drafts), hs2_full_attn_accumulate_each()
+ * takes one for each.  Only the weights of q are added: those of queries that
+ * hs2_tree_attn() verified reach no sum.  Positions t >= T_b are not touched.
  *
  *   acc        device fp32 [B, Hkv] rows of acc_stride >= t_cap elements.
  *   Other arguments, the workspace (hs2_full_attn_select_workspace()) and limits as for
@@ -384,6 +388,15 @@ int hs2_full_attn_accumulate(const hs2_heads *q, const hs2_cache *k_cache, const
                              const int32_t *seq_lens, const int32_t *page_table, int32_t max_pages, float decay,
                              int32_t fresh, float *acc, int64_t acc_stride, hs2_heads *out, void *workspace,
                              size_t workspace_bytes, void *stream);
+
+/*
+ * hs2_full_attn_accumulate() with a number of new positions for every sequence:
+ *   fresh      device int32 [B], clamped to [0, T_b]; after hs2_tree_accept() its path_len.
+ */
+int hs2_full_attn_accumulate_each(const hs2_heads *q, const hs2_cache *k_cache, const hs2_cache *v_cache,
+                                  const int32_t *seq_lens, const int32_t *page_table, int32_t max_pages, float decay,
+                                  const int32_t *fresh, float *acc, int64_t acc_stride, hs2_heads *out,
+                                  void *workspace, size_t workspace_bytes, void *stream);
 
 /*
  * Eviction: where T_b > budget, every kv head keeps its newest `window` positions

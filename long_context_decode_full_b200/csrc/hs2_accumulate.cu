@@ -2,8 +2,8 @@
 //
 // After the attention kernel has left the raw logits s_{h,t} and the segment
 // records, acc[t] = decay * acc[t] + sum_h 2^(a s_{h,t} - b_h) with a = c
-// log2(e) and b_h = LSE_h log2(e); the newest `fresh` tokens start at their
-// first weight.  a and b_h are carried as float pairs, so the exponent's one
+// log2(e) and b_h = LSE_h log2(e); the newest `fresh` tokens (of each sequence, as
+// many as it has gained since the last call) start at their first weight.  a and b_h are carried as float pairs, so the exponent's one
 // rounding of consequence is the fused multiply-add's (below 2^-20 for weights
 // above 2^-16).
 //
@@ -57,6 +57,7 @@ __global__ void __launch_bounds__(kAccThreads) accumulate_kernel(const Accumulat
   }
   const float *lg = p.ws.logits + (size_t)u * p.ustride * G;
   float *acc = ap.acc + (size_t)u * ap.acc_stride;
+  const int old_end = ui.T - (ap.fresh_each ? clamp_len(__ldg(ap.fresh_each + b), ui.T) : ap.fresh);  // sums below go on
   constexpr int Q = G >= 16 ? 1 : (G >= 8 ? 2 : 4);  // positions of a thread in flight
   for (int tb = t0 + (int)threadIdx.x; tb < t1; tb += Q * kAccThreads) {
     float raw[Q][G], old[Q];
@@ -65,7 +66,7 @@ __global__ void __launch_bounds__(kAccThreads) accumulate_kernel(const Accumulat
       const int t = tb + q * kAccThreads;
       old[q] = 0.f;
       if (t >= t1) continue;
-      if (t < ui.T - ap.fresh) old[q] = __ldcs(acc + t);
+      if (t < old_end) old[q] = __ldcs(acc + t);
       if constexpr (G % 4 == 0) {
 #pragma unroll
         for (int h4 = 0; h4 < G / 4; ++h4) {
@@ -94,7 +95,7 @@ __global__ void __launch_bounds__(kAccThreads) accumulate_kernel(const Accumulat
       for (int s = 1; s < G; s <<= 1)
 #pragma unroll
         for (int h = 0; h + s < G; h += 2 * s) w[h] += w[h + s];
-      acc[t] = t < ui.T - ap.fresh ? fmaf(ap.decay, old[q], w[0]) : w[0];
+      acc[t] = t < old_end ? fmaf(ap.decay, old[q], w[0]) : w[0];
     }
   }
 }

@@ -393,6 +393,20 @@ int hs2_full_attn_accumulate(const hs2_heads *q, const hs2_cache *k_cache, const
                                workspace_bytes, stream, nullptr, false, &ap);
 }
 
+int hs2_full_attn_accumulate_each(const hs2_heads *q, const hs2_cache *k_cache, const hs2_cache *v_cache,
+                                  const int32_t *seq_lens, const int32_t *page_table, int32_t max_pages, float decay,
+                                  const int32_t *fresh, float *acc, int64_t acc_stride, hs2_heads *out,
+                                  void *workspace, size_t workspace_bytes, void *stream) {
+  if (!fresh) return fail(HS2_ERR_INVALID_ARG, "fresh is NULL");
+  AccumulateParams ap{};
+  ap.acc = acc;
+  ap.acc_stride = acc_stride;
+  ap.decay = decay;
+  ap.fresh_each = fresh;
+  return full_attn_select_impl(q, k_cache, v_cache, seq_lens, page_table, max_pages, 0, 0, 0, out, nullptr, workspace,
+                               workspace_bytes, stream, nullptr, false, &ap);
+}
+
 }  // extern "C"
 
 namespace {

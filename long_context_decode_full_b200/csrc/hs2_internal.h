@@ -246,7 +246,8 @@ struct AccumulateParams {
   float *acc;
   int64_t acc_stride;
   float decay;
-  int32_t fresh;                     // the newest tokens, whose sums start at this call
+  int32_t fresh;                     // the newest tokens, whose sums start at this call,
+  const int32_t *fresh_each;         // or [B]: their number in each sequence
 };
 cudaError_t launch_accumulate(const AccumulateParams &p, cudaStream_t s);
 // its attention over an fp32 cache, in tiles of full_f32_tile() positions

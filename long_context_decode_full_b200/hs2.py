@@ -62,7 +62,7 @@ EXPORTS = ["hs2_full_attn_select_workspace", "hs2_full_attn_select", "hs2_full_a
            "hs2_workspace_status", "hs2_selftest_bounded_wait", "hs2_selftest_grid_barrier",
            "hs2_kv_bridge_workspace", "hs2_kv_bridge_append",
            "hs2_rope_table", "hs2_rope_append", "hs2_tree_attn_workspace", "hs2_tree_attn", "hs2_tree_accept",
-           "hs2_full_attn_accumulate", "hs2_cache_evict",
+           "hs2_full_attn_accumulate", "hs2_full_attn_accumulate_each", "hs2_cache_evict",
            "hs2_copy_peak", "hs2_last_error", "hs2_version"]
 
 
@@ -119,6 +119,9 @@ def lib():
         L.hs2_full_attn_accumulate.argtypes = [ctypes.POINTER(Heads), C, C, P, P, I32, F, I32, P, I64,
                                                ctypes.POINTER(Heads), P, SZ, P]
         L.hs2_full_attn_accumulate.restype = ctypes.c_int
+        L.hs2_full_attn_accumulate_each.argtypes = [ctypes.POINTER(Heads), C, C, P, P, I32, F, P, P, I64,
+                                                    ctypes.POINTER(Heads), P, SZ, P]
+        L.hs2_full_attn_accumulate_each.restype = ctypes.c_int
         L.hs2_cache_evict.argtypes = [C, C, P, I32, P, I32, P, I64, I32, I32, P, P, P]
         L.hs2_cache_evict.restype = ctypes.c_int
         L.hs2_selftest_bounded_wait.argtypes = [P, SZ, P]
@@ -498,7 +501,7 @@ _current_device, _raw_stream = torch.cuda.current_device, getattr(
 _ROPE_NAMES = ("v", "q", "k_new", "v_new", "positions", "table", "seq_lens", "num_new", "page_table", "k_scale", "v_scale", "q_out")
 _TREE_NAMES = ("v", "q", "out", "tree_mask", "seq_lens", "num_draft", "page_table", "k_scale", "v_scale", "workspace")
 _ACCEPT_NAMES = ("v", "seq_lens", "path", "path_len", "num_draft", "page_table", "k_scale", "v_scale", "lens_out")
-_ACCUMULATE_NAMES = ("v", "q", "seq_lens", "acc", "page_table", "k_scale", "v_scale", "out", "workspace")
+_ACCUMULATE_NAMES = ("v", "q", "seq_lens", "acc", "fresh", "page_table", "k_scale", "v_scale", "out", "workspace")
 _EVICT_NAMES = ("v", "seq_lens", "acc", "page_table", "k_scale", "v_scale", "kept", "lens_out")
 
 
@@ -616,7 +619,8 @@ def _sums(acc, B, Hkv):
 def full_attn_accumulate(q, k, v, seq_lens, acc, page_table=None, page_size=None, decay=1.0, fresh=1, k_scale=None,
                          v_scale=None, out=None, workspace=None, stream=None):
     """The full layer's attention, its weights added to the running sums acc [B, Hkv, >= capacity] (fp32):
-    acc = decay * acc + weights, the newest ``fresh`` positions starting anew.  Returns (out, acc)."""
+    acc = decay * acc + weights, the newest ``fresh`` positions starting anew: as many as each sequence gained since the
+    last call, a number for all or int32 [B] (after tree_accept(), its path_len).  Returns (out, acc)."""
     _need("q", q, _q_dtype(k), dim=3)
     B, Hq, d = q.shape
     lp = _arg("seq_lens", seq_lens, torch.int32, (B,))
@@ -626,13 +630,17 @@ def full_attn_accumulate(q, k, v, seq_lens, acc, page_table=None, page_size=None
         with _on(stream):
             out = torch.empty_like(q)
     _arg("out", out, q.dtype, q.shape)
-    device = _device(_ACCUMULATE_NAMES, k, v, q, seq_lens, acc, page_table, k_scale, v_scale, out, workspace)
+    each = fresh if torch.is_tensor(fresh) else None
+    call, new = lib().hs2_full_attn_accumulate, fresh
+    if each is not None:
+        call, new = lib().hs2_full_attn_accumulate_each, _arg("fresh", each, torch.int32, (B,))
+    device = _device(_ACCUMULATE_NAMES, k, v, q, seq_lens, acc, each, page_table, k_scale, v_scale, out, workspace)
     if workspace is None:
         with torch.cuda.device(device), _on(stream):
             workspace = alloc_workspace(B, k.shape[1], Hq // k.shape[1], d, kc.page_size * max_pages, k.device)
     _need("workspace", workspace, torch.uint8)
-    _run(lib().hs2_full_attn_accumulate, device, stream, heads_desc(q), kc, vc, lp, pages, max_pages, decay, fresh, sums,
-         cap, heads_desc(out), workspace.data_ptr(), workspace.numel())
+    _run(call, device, stream, heads_desc(q), kc, vc, lp, pages, max_pages, decay, new, sums, cap,
+         heads_desc(out), workspace.data_ptr(), workspace.numel())
     return out, acc
 
 

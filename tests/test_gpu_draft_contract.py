@@ -1,6 +1,8 @@
 """What the drafted-token and bounded-cache calls promise beside their formulas: where results and workspaces are made,
 counts of each sequence's own, paths narrower than the draft, codes that both appends write, rows and sums that nothing
 may read.  Plain 64-bit forms in tests/draft_ref.py."""
+import math
+
 import pytest
 import torch
 
@@ -9,6 +11,7 @@ from test_gpu_draft import check, gen, i32, tree_case
 from long_context_decode_full_b200 import hs2
 
 pytestmark = pytest.mark.gpu
+NAN = float("nan")
 BUSY = 100_000_000  # cycles, some 50 ms: longer than any call here
 
 
@@ -119,3 +122,37 @@ def test_tree_attn_graphs_that_share_a_workspace(dtype):
     assert hs2.workspace_status(ws[:n]) == hs2.OK
     each()
     assert bool((ws[n:] == 0x5A).all())
+
+
+# ---------------------------------------------------------------- running sums
+def weights(c, q, b, h, G, d):
+    """Summed softmax probabilities of a group, and their error's bound relative to them: logits in fp32 sums, the
+    exponent's rounding 2^-20 and the exponential 2^-21, G additions (R.attend() and the update kernel)."""
+    k = c.wide("k", b, torch.arange(c.T[b]))[:, h]
+    rows = q[b, h * G:(h + 1) * G].double()
+    e = (d + 2) * 2.0 ** -24 * float((rows.abs() @ k.abs().T).amax()) / math.sqrt(d)
+    return torch.softmax(rows @ k.T / math.sqrt(d), -1).sum(0), 2 * e + 2.0 ** -12 + (G + 2) * 2.0 ** -24
+
+
+@pytest.mark.parametrize("dtype,G,page", [("bf16", 8, 64), ("e4m3", 4, 16), ("f32", 2, 0), ("bf16", 16, 32), ("f32", 8, 16)])
+def test_accumulate_starts_each_sequences_own_new_tokens(dtype, G, page):
+    """Sequences that gained different counts: the sums of each one's newest tokens start, all others are kept."""
+    hkv, d, decay = 2, 128, 0.75
+    lens, gained = [700, 77, 150, 0, 4099, 33, 5], [5, 0, 150, 3, 2 ** 31 - 1, 1, -4]
+    c = R.PagedCache(dtype, lens, hkv, d, page, seed=51)
+    q = torch.randn(len(lens), hkv * G, d, device="cuda", generator=gen(52)).to(R.q_dtype(dtype))
+    acc0 = torch.rand(len(lens), hkv, c.cap, device="cuda", generator=gen(53)) * 5
+    fresh = [max(0, min(n, T)) for n, T in zip(gained, lens)]
+    for b, T in enumerate(lens):
+        acc0[b, :, T - fresh[b]:] = NAN  # not read
+    acc = acc0.clone()
+    hs2.full_attn_accumulate(q, c.k, c.v, c.lens, acc, decay=decay, fresh=i32(gained), **c.kw())
+    for b, T in enumerate(lens):
+        for h in range(hkv):
+            if T:
+                w, slack = weights(c, q, b, h, G, d)
+                old = acc0[b, h, :T].double() * decay
+                old[T - fresh[b]:] = 0
+                err = (acc[b, h, :T].double() - old - w).abs()
+                assert bool((err <= slack * w + 2.0 ** -22 * old + 1e-30).all()), (b, h)
+            assert torch.equal(R.bits(acc[b, h, T:]), R.bits(acc0[b, h, T:]))
