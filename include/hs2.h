@@ -357,8 +357,10 @@ int hs2_tree_attn(const hs2_tokens *q, const hs2_cache *k_cache, const hs2_cache
  *   path       device int32 [batch, max_path], max_path in [1, 64]: indices of the accepted
  *              drafts, in the order in which they continue the context (any order: every row
  *              is read before one is written).  An index outside [0, n_b) moves nothing.
- *   path_len   device int32 [batch], clamped to [0, n_b].
- *   num_draft  device int32 [batch]: n_b, clamped to [0, min(max_path, T_b)]; NULL: max_path for all.
+ *              The paths may be narrower than the draft.
+ *   path_len   device int32 [batch], clamped to [0, min(n_b, max_path)].
+ *   num_draft  device int32 [batch]: n_b, as given to hs2_tree_attn(), clamped to [0, min(64, T_b)];
+ *              NULL: max_path for all.
  *   lens_out   device int32 [batch], apart from seq_lens, num_draft and path_len.
  * The rows behind the new length are not defined.  Asynchronous; needs no workspace.
  */

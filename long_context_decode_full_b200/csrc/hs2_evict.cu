@@ -38,8 +38,8 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_kernel(const AcceptPara
   griddep_launch_dependents();
   const int b = blockIdx.y, job = blockIdx.x;
   const int T = clamp_len(__ldg(p.seq_lens + b), (int)p.t_cap);
-  const int n = clamp_len(p.num_draft ? __ldg(p.num_draft + b) : p.M, min(min(p.M, kMaxDraft), T));
-  const int a = clamp_len(__ldg(p.path_len + b), n);
+  const int n = clamp_len(p.num_draft ? __ldg(p.num_draft + b) : p.M, min(kMaxDraft, T));  // a path may be narrower
+  const int a = clamp_len(__ldg(p.path_len + b), min(n, p.M));
   const int first = T - n;
   if ((int)threadIdx.x < a) {
     const int j = __ldg(p.path + (int64_t)b * p.M + threadIdx.x);

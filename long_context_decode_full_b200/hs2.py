@@ -590,8 +590,9 @@ def tree_attn(q, k, v, seq_lens, page_table=None, page_size=None, tree_mask=None
 
 def tree_accept(k, v, seq_lens, path, path_len, page_table=None, page_size=None, num_draft=None, k_scale=None,
                 v_scale=None, lens_out=None, stream=None):
-    """After a verification: the rows of the accepted drafts path[b, :path_len[b]] move to the front of the draft.
-    Returns the new lengths."""
+    """After a verification: the rows of the accepted drafts path[b, :path_len[b]] move to the front of the draft, whose
+    size is num_draft[b] (None: the width of ``path``, so a path narrower than the draft needs it).  Returns the new
+    lengths."""
     if path.dim() != 2:
         _need("path", path, torch.int32, dim=2)
     B, M = path.shape

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import draft_ref as R
-from test_gpu_draft import check, gen, i32, tree_case
+from test_gpu_draft import check, gen, i32, random_tree, tree_case
 from long_context_decode_full_b200 import hs2
 
 pytestmark = pytest.mark.gpu
@@ -124,6 +124,32 @@ def test_tree_attn_graphs_that_share_a_workspace(dtype):
     assert bool((ws[n:] == 0x5A).all())
 
 
+# ---------------------------------------------------------------- accepted paths
+@pytest.mark.parametrize("dtype,width", [("bf16", 5), ("e4m3", 1), ("f32", 17)])
+def test_tree_accept_path_narrower_than_the_draft(dtype, width):
+    """A path of a few drafts out of a tree of many: the draft's size is num_draft, not the path's width."""
+    lens, drafts = [500, 64, 129, 30], [64, 64, 40, 30]
+    plen = [width, min(3, width), width + 9, 0]
+    c = R.PagedCache(dtype, lens, 2, 128, 16, seed=3)
+    g = torch.Generator().manual_seed(2)
+    path = torch.stack([torch.randperm(n, generator=g)[:width].sort().values for n in (64, 64, 40, 30)]).to(torch.int32)
+    before = c.snapshot()
+    got = hs2.tree_accept(c.k, c.v, c.lens, path.cuda(), i32(plen), num_draft=i32(drafts), **c.kw())
+    want = [None if x is None else x.clone() for x in before]
+    new = []
+    for b, (T, n) in enumerate(zip(lens, drafts)):
+        a = min(plen[b], width, n)
+        new.append(T - n + a)
+        for i in range(a):
+            src, dst = int(c.slots(b, T - n + int(path[b, i]))), int(c.slots(b, T - n + i))
+            for x, y in zip(want, before):
+                if x is not None:
+                    x[dst] = y[src]
+    assert got.tolist() == new
+    for x, y in zip((c.k, c.v, c.k_scale, c.v_scale), want):
+        assert x is None or torch.equal(R.bits(x), R.bits(y))
+
+
 # ---------------------------------------------------------------- running sums
 def weights(c, q, b, h, G, d):
     """Summed softmax probabilities of a group, and their error's bound relative to them: logits in fp32 sums, the
@@ -156,3 +182,58 @@ def test_accumulate_starts_each_sequences_own_new_tokens(dtype, G, page):
                 err = (acc[b, h, :T].double() - old - w).abs()
                 assert bool((err <= slack * w + 2.0 ** -22 * old + 1e-30).all()), (b, h)
             assert torch.equal(R.bits(acc[b, h, T:]), R.bits(acc0[b, h, T:]))
+
+
+# ---------------------------------------------------------------- together
+@pytest.mark.parametrize("dtype,page", [("bf16", 16), ("e4m3", 64), ("f32", 0)])
+def test_verify_accumulate_evict_reads_no_undefined_sum(dtype, page):
+    """The sequence of the documentation: a drafted tree, its accepted path, the full layer with running sums, eviction.
+    Sums behind a sequence's length are NaN before every step; none may reach a sum that counts."""
+    hkv, G, d, N, B, budget, window, decay = 2, 4, 128, 6, 3, 40, 8, 0.9
+    T = [38, 9, 60]
+    c = R.PagedCache(dtype, T, hkv, d, page, seed=61, spare=40, poison=False)
+    acc = torch.rand(B, hkv, c.cap, device="cuda", generator=gen(62))
+    table, seen = hs2.rope_table(128), list(T)
+    g = torch.Generator().manual_seed(63)
+    for step in range(4):
+        for b in range(B):
+            acc[b, :, T[b]:] = NAN
+        parents = [random_tree(N, 7 * step + b) for b in range(B)]
+        nd = [N, 1 + step, N - 1]
+        qkv = torch.randn(B, N, hkv * (G + 2), d, device="cuda", generator=gen(70 + step)).to(R.q_dtype(dtype))
+        T = [t + n for t, n in zip(T, nd)]
+        c.T, c.lens = T, i32(T)
+        pos = i32([[s + i for i in range(N)] for s in seen])
+        q = hs2.rope_append(qkv[:, :, :hkv * G], qkv[:, :, hkv * G:hkv * (G + 1)], qkv[:, :, hkv * (G + 1):], pos, table,
+                            c.k, c.v, c.lens, num_new=i32(nd), **c.kw())
+        hs2.tree_attn(q, c.k, c.v, c.lens, tree_mask=hs2.tree_mask(parents).cuda(), num_draft=i32(nd), **c.kw())
+        path = []
+        for b in range(B):
+            i, p = int(torch.randint(0, nd[b], (), generator=g)), []
+            while i >= 0:
+                p.append(i)
+                i = parents[b][i]
+            path.append(p[::-1])
+        plen, width = [len(p) for p in path], max(len(p) for p in path)
+        c.lens = hs2.tree_accept(c.k, c.v, c.lens, i32([p + [0] * (width - len(p)) for p in path]), i32(plen), num_draft=i32(nd), **c.kw())
+        T = [t - n + a for t, n, a in zip(T, nd, plen)]
+        assert c.lens.tolist() == T
+        c.T, seen = T, [s + a for s, a in zip(seen, plen)]
+        q1 = torch.stack([q[b, path[b][-1]] for b in range(B)])
+        acc0 = acc.clone()
+        hs2.full_attn_accumulate(q1, c.k, c.v, c.lens, acc, decay=decay, fresh=i32(plen), **c.kw())
+        for b in range(B):
+            for h in range(hkv):
+                w, slack = weights(c, q1, b, h, G, d)
+                old = acc0[b, h, :T[b]].double() * decay
+                old[T[b] - plen[b]:] = 0
+                err = (acc[b, h, :T[b]].double() - old - w).abs()
+                assert bool((err <= slack * w + 2.0 ** -22 * old + 1e-30).all()), (step, b, h)
+        sums = acc.clone()
+        c.lens, kept = hs2.cache_evict(c.k, c.v, c.lens, acc, budget, window, **c.kw())
+        for b in range(B):
+            for h in range(hkv):
+                keep = R.kept_positions(sums[b, h, :T[b]].tolist(), T[b], budget, window)
+                assert kept[b, h, :len(keep)].tolist() == keep
+        c.T = T = c.lens.tolist()
+    assert max(T) == budget
