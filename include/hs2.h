@@ -308,7 +308,8 @@ int hs2_rope_table(const hs2_rope *rope, uint64_t *table, float *rot_scale);
  * the angle reduced exactly at any position.  Pairs are (e, e + rot_dim / 2), or
  * (2e, 2e + 1) with `interleaved`.  Queries go to q_out; keys and the values (not
  * rotated) are written at positions T_b - n_b + i of the caches as
- * hs2_kv_bridge_append() writes them: fp32, bf16, or E4M3 with scale = max / 448.
+ * hs2_kv_bridge_append() writes them: fp32, bf16, or E4M3 with scale = max / 448 and the
+ * same codes (here the scale is 1 also where max / 448 underflows to 0).
  *
  *   q          [B, N, Hq, d] or NULL (then q_out is NULL: keys and values only).
  *   k, v       [B, N, Hkv, d].

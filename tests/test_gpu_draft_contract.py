@@ -237,3 +237,50 @@ def test_verify_accumulate_evict_reads_no_undefined_sum(dtype, page):
                 assert kept[b, h, :len(keep)].tolist() == keep
         c.T = T = c.lens.tolist()
     assert max(T) == budget
+
+
+# ---------------------------------------------------------------- E4M3 rows
+def test_rope_append_and_kv_bridge_append_write_the_same_e4m3_rows():
+    """The same bf16 rows through both appends: codes and scales equal, where x / scale lies next to the middle of two
+    codes (x = a maximum's 448th times such a middle), among random, tiny and huge rows."""
+    hkv, d, dm = 1, 128, 384
+    rows = torch.randn(dm, d, generator=torch.Generator().manual_seed(81)).to(torch.bfloat16).double()
+    middles = [m * 2.0 ** k for k in range(-9, 5) for m in (17, 19, 21, 23, 25, 27, 29, 31)]
+    for a in range(1, 256):  # the maximum a / 256; elements that are bf16 and exactly in the middle, up to the scale's rounding
+        x = [a / 256 * m / 448 for m in middles]
+        x = [v for v in x if float(torch.tensor(v).to(torch.bfloat16)) == v and v <= a / 256]
+        rows[a, 0] = a / 256
+        rows[a, 1:] *= a / 256 / rows[a, 1:].abs().max()
+        rows[a] = rows[a].to(torch.bfloat16).double()
+        rows[a, 1:1 + len(x)] = torch.tensor(x[:d - 1], dtype=torch.float64) * torch.where(torch.arange(len(x[:d - 1])) % 2 > 0, -1.0, 1.0)
+    for i, size in enumerate([2.0 ** -120, 2.0 ** -100, 2.0 ** -70, 2.0 ** -60, 2.0 ** -59, 2.0 ** 60, 2.0 ** 120]):
+        rows[300 + i] = rows[85] * size
+    rows[310] = 0
+    w = rows.to(torch.bfloat16).cuda()
+    hidden = torch.eye(dm, device="cuda", dtype=torch.bfloat16)  # sequence b's row is row b of w
+    caches = [R.PagedCache("e4m3", [1] * dm, hkv, d, 16, seed=82, spare=3) for _ in (0, 1)]
+    a, b = caches
+    hs2.kv_bridge_append(hidden, w, w, a.k, a.v, a.lens, **a.kw())
+    x = w.view(dm, 1, hkv, d)
+    hs2.rope_append(None, x, x, torch.zeros(dm, 1, dtype=torch.int32, device="cuda"), hs2.rope_table(128), b.k, b.v, b.lens, **b.kw())
+    # an element of -0 is 0 in the product's sum, which starts from +0: zeros of either sign are equal
+    code = lambda t: torch.where(R.bits(t) == 0x80, torch.zeros_like(R.bits(t)), R.bits(t))  # noqa: E731
+    assert torch.equal(code(a.k), code(b.k)) and torch.equal(code(a.v), code(b.v))
+    assert torch.equal(R.bits(a.k_scale), R.bits(b.k_scale)) and torch.equal(R.bits(a.v_scale), R.bits(b.v_scale))
+
+
+def test_rope_append_e4m3_codes_are_the_quotients():
+    """Codes of many rows of all sizes against fp32 divisions by the stored scale, bit for bit."""
+    B, N, hkv, d = 4, 257, 8, 128
+    x = torch.randn(B, N, hkv, d, device="cuda", generator=gen(91))
+    x *= torch.exp2(torch.randint(-130, 120, (B, N, hkv, 1), device="cuda", generator=gen(92)).float())
+    x = x.bfloat16()
+    c = R.PagedCache("e4m3", [N] * B, hkv, d, 64, seed=93)
+    hs2.rope_append(None, x, x, torch.zeros(B, N, dtype=torch.int32, device="cuda"), hs2.rope_table(64), c.k, c.v, c.lens, **c.kw())
+    top = x.float().abs().amax(-1)
+    scale = top / torch.full_like(top, 448.0)  # by a tensor: a number's reciprocal would be multiplied
+    scale = torch.where(scale > 0, scale, torch.ones_like(scale))
+    codes = (x.float() / scale.unsqueeze(-1)).clamp(-448, 448).to(torch.float8_e4m3fn)
+    for b in range(B):
+        s = c.slots(b, torch.arange(N))
+        assert torch.equal(c.v_scale[s], scale[b]) and torch.equal(R.bits(c.v[s]), R.bits(codes[b]))
