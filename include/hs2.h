@@ -326,7 +326,8 @@ int hs2_rope_append(const hs2_tokens *q, const hs2_tokens *k, const hs2_tokens *
                     const int32_t *seq_lens, const int32_t *num_new, const int32_t *page_table, int32_t max_pages,
                     const hs2_cache *k_cache, const hs2_cache *v_cache, void *q_out, void *stream);
 
-/* Workspace bytes of hs2_tree_attn() for this shape on the current device (0 if invalid). */
+/* Workspace bytes of hs2_tree_attn() for this shape on the current device (0 if invalid);
+ * enough for every call of as many or fewer tokens and sequences. */
 size_t hs2_tree_attn_workspace(int32_t batch, int32_t tokens, int32_t num_kv_heads, int32_t group, int32_t head_dim,
                                int32_t kv_dtype);
 

@@ -38,15 +38,15 @@ struct TreePlan {
   size_t prefix, records, total;
 };
 
-// t_cap: the capacity per sequence (fp32 caches: short tiles where long ones are too few)
-TreePlan tree_plan(int B, int N, int Hkv, int G, int D, bool f32, int64_t t_cap) {
+// `small`: the small tiles, where the call's shape has them (fp32 caches, 32 rows)
+TreePlan tree_plan(int B, int N, int G, int D, bool f32, bool small) {
   TreePlan t{};
   t.tile = tree_tc_tile();
   t.rows = tree_tc_rows();
   t.streams = f32 ? 1 : 2;
   if (f32) {  // two blocks of few rows take 0.6 to 1.06 of the tiled kernel's time, three would take as long as it
     t.rows = N * G <= 2 * tree_f32_few_rows() ? tree_f32_few_rows() : (N * G <= 32 ? 32 : 64);
-    t.tile = t.rows == 32 && (t_cap + 63) / 64 * Hkv * B < sm_count() ? 32 : 64;
+    t.tile = t.rows == 32 && small ? 32 : 64;
   }
   const int ctas = sm_count() * (f32 ? tree_f32_ctas_per_sm(D, t.rows, t.tile) : 1), per_block = t.rows * t.streams;
   t.blocks = (N * G + per_block - 1) / per_block;
@@ -176,11 +176,16 @@ size_t hs2_tree_attn_workspace(int32_t batch, int32_t tokens, int32_t num_kv_hea
   if (batch < 1 || batch > kMaxBatchSmem || tokens < 1 || tokens > kMaxDraft || num_kv_heads < 1 || !group_ok(group) ||
       (head_dim != 64 && head_dim != 128) || kv_dtype < HS2_F32 || kv_dtype > HS2_E4M3)
     return 0;
-  // the larger of the plans that the call may choose by its capacity
+  // The most that a call of this many tokens and sequences or fewer needs, at any capacity: shorter drafts have fewer
+  // row blocks and so more shares.
   const bool f32 = kv_dtype == HS2_F32;
-  const size_t a = tree_plan(batch, tokens, num_kv_heads, group, head_dim, f32, 1).total;
-  const size_t b = tree_plan(batch, tokens, num_kv_heads, group, head_dim, f32, kMaxContext).total;
-  return a > b ? a : b;
+  size_t most = 0;
+  for (int n = 1; n <= tokens; ++n)
+    for (const bool small : {false, true}) {
+      const size_t t = tree_plan(batch, n, group, head_dim, f32, small).total;
+      most = t > most ? t : most;
+    }
+  return most;
 }
 
 int hs2_tree_attn(const hs2_tokens *q, const hs2_cache *k_cache, const hs2_cache *v_cache, const int32_t *seq_lens,
@@ -207,7 +212,9 @@ int hs2_tree_attn(const hs2_tokens *q, const hs2_cache *k_cache, const hs2_cache
   if (k_cache->dtype != HS2_F32 && page_table && !(ps % 16 == 0 && (ps % 64 == 0 || 64 % ps == 0)))
     return fail(HS2_ERR_UNSUPPORTED, "page_size %d (16, 32 or a multiple of 64)", ps);
   const bool f32 = k_cache->dtype == HS2_F32;
-  const TreePlan plan = tree_plan(q->batch, q->tokens, Hkv, G, D, f32, t_cap);
+  // short tiles where long ones are too few for the SMs
+  const bool small = (t_cap + 63) / 64 * Hkv * q->batch < sm_count();
+  const TreePlan plan = tree_plan(q->batch, q->tokens, G, D, f32, small);
   if (!workspace) return fail(HS2_ERR_WORKSPACE, "workspace is NULL");
   if (reinterpret_cast<uintptr_t>(workspace) & 255) return fail(HS2_ERR_WORKSPACE, "workspace not 256-byte aligned");
   if (workspace_bytes < plan.total)

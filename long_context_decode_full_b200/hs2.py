@@ -553,7 +553,7 @@ def tree_workspace_bytes(batch: int, tokens: int, num_kv_heads: int, group: int,
 
 
 def alloc_tree_workspace(q, k) -> torch.Tensor:
-    """A workspace for tree_attn() of queries like q [B, N, Hq, d] over caches like k."""
+    """A workspace for tree_attn() of queries like q [B, N, Hq, d] over caches like k, or of fewer sequences or tokens."""
     B, N, Hq, d = q.shape
     with torch.cuda.device(k.device):
         n = tree_workspace_bytes(B, N, k.shape[1], Hq // k.shape[1], d, _DTYPE[k.dtype])

@@ -27,3 +27,17 @@ def test_fresh_counts_are_checked(libhs2):
     for fresh, word in ((lens.long(), "dtype"), (lens[:1], "shape"), (lens.view(2, 1), "shape")):
         with pytest.raises(hs2.HS2Error, match=f"fresh: {word}"):
             hs2.full_attn_accumulate(q, k, k.clone(), lens, acc, fresh=fresh)
+
+
+# ---------------------------------------------------------------- workspaces
+@pytest.mark.parametrize("dtype,groups,dims", [(0, (1, 2, 4, 8), (64, 128)), (1, (1, 2, 8, 16, 32), (64, 128)), (2, (1, 8, 32), (128,))])
+def test_tree_workspace_serves_every_smaller_call(libhs2, dtype, groups, dims):
+    """A server that sizes its workspace for the longest draft and the largest batch: no smaller call asks for more."""
+    for group in groups:
+        for dim in dims:
+            for heads in (1, 4):
+                size = lambda b, n: hs2.tree_workspace_bytes(b, n, heads, group, dim, dtype)  # noqa: B023, E731
+                for tokens in (1, 2, 5, 8, 16, 33, 64):
+                    for batch in (1, 8, 64, 500):
+                        most = size(batch, tokens)
+                        assert all(size(b, n) <= most for b in (1, 2, batch) for n in range(1, tokens + 1) if b <= batch)

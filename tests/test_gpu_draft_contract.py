@@ -124,6 +124,20 @@ def test_tree_attn_graphs_that_share_a_workspace(dtype):
     assert bool((ws[n:] == 0x5A).all())
 
 
+# ---------------------------------------------------------------- one workspace for drafts of all lengths
+@pytest.mark.parametrize("dtype,hkv,G,d,N", [("bf16", 1, 32, 128, 8), ("f32", 1, 8, 128, 4), ("f32", 4, 4, 64, 5), ("e4m3", 2, 8, 128, 3)])
+def test_tree_attn_short_drafts_in_a_long_drafts_workspace(dtype, hkv, G, d, N):
+    most = R.PagedCache(dtype, [64] * 40, hkv, d, 64, seed=1)
+    ws = hs2.alloc_tree_workspace(torch.empty(40, 64, hkv * G, d, device="cuda", dtype=R.q_dtype(dtype)), most.k)
+    for lens in ([3000], [700, N, 65]):
+        case = (dtype, hkv, G, d, 64, N, lens, [N] * len(lens))
+        c, q, masks, words = tree_case(*case, seed=15)
+        out = torch.full_like(q, 77.0)
+        hs2.tree_attn(q, c.k, c.v, c.lens, tree_mask=words, out=out, workspace=ws, **c.kw())
+        want, bound = R.tree_reference(c, q, [N] * len(lens), masks, dtype)
+        check(out, want, bound, ~want.isnan())
+
+
 # ---------------------------------------------------------------- accepted paths
 @pytest.mark.parametrize("dtype,width", [("bf16", 5), ("e4m3", 1), ("f32", 17)])
 def test_tree_accept_path_narrower_than_the_draft(dtype, width):
