@@ -645,16 +645,19 @@ def full_attn_accumulate(q, k, v, seq_lens, acc, page_table=None, page_size=None
     return out, acc
 
 
-def cache_evict(k, v, seq_lens, acc, budget, window=128, page_table=None, page_size=None, k_scale=None, v_scale=None,
+def cache_evict(k, v, seq_lens, acc, budget, window=None, page_table=None, page_size=None, k_scale=None, v_scale=None,
                 kept=None, lens_out=None, stream=None):
-    """Where a sequence is longer than ``budget``, every kv head keeps its newest ``window`` tokens and the
-    budget - window others with the largest sums in acc [B, Hkv, >= capacity]; their rows, scales and sums move to the
-    front, in order and in place.  Returns (lens_out [B], kept [B, Hkv, budget]: the kept positions, -1 padded)."""
+    """Where a sequence is longer than ``budget``, every kv head keeps its newest ``window`` tokens (None: 128, or the
+    whole of a smaller budget) and the budget - window others with the largest sums in acc [B, Hkv, >= capacity]; their
+    rows, scales and sums move to the front, in order and in place.  Returns (lens_out [B], kept [B, Hkv, budget]: the
+    kept positions, -1 padded)."""
     _need("seq_lens", seq_lens, torch.int32, dim=1)
     B, lp = seq_lens.shape[0], seq_lens.data_ptr()
     kc, vc, pages, max_pages = _paged(k, v, k_scale, v_scale, page_table, page_size, B)
     Hkv = k.shape[1]
     cap, sums = _sums(acc, B, Hkv)
+    if window is None:
+        window = min(128, budget)
     with _on(stream):
         if kept is None:
             kept = torch.empty(B, Hkv, max(budget, 0), dtype=torch.int32, device=k.device)

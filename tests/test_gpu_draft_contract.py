@@ -253,6 +253,19 @@ def test_verify_accumulate_evict_reads_no_undefined_sum(dtype, page):
     assert max(T) == budget
 
 
+# ---------------------------------------------------------------- eviction
+@pytest.mark.parametrize("budget", [64, 128, 200])
+def test_cache_evict_default_window(budget):
+    """Without a window given: 128 tokens, or the whole of a smaller budget."""
+    cases = [R.PagedCache("bf16", [500, 50], 2, 128, 16, seed=71) for _ in (0, 1)]
+    acc = torch.rand(2, 2, cases[0].cap, device="cuda", generator=gen(72))
+    got = hs2.cache_evict(cases[0].k, cases[0].v, cases[0].lens, acc.clone(), budget, **cases[0].kw())
+    want = hs2.cache_evict(cases[1].k, cases[1].v, cases[1].lens, acc.clone(), budget, min(128, budget), **cases[1].kw())
+    for x, y in zip(got, want):
+        assert torch.equal(x, y)
+    assert torch.equal(R.bits(cases[0].k), R.bits(cases[1].k))
+
+
 # ---------------------------------------------------------------- E4M3 rows
 def test_rope_append_and_kv_bridge_append_write_the_same_e4m3_rows():
     """The same bf16 rows through both appends: codes and scales equal, where x / scale lies next to the middle of two
