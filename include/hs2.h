@@ -319,6 +319,8 @@ int hs2_rope_table(const hs2_rope *rope, uint64_t *table, float *rot_scale);
  *   num_new    device int32 [B]: n_b, clamped to [0, min(N, T_b)]; NULL: N for all.
  *   q_out      device [B, N, Hq, d], contiguous, dtype of q; may be q->data when q is
  *              contiguous.  Rows of tokens i >= n_b are not touched.
+ * The K and V caches lie apart, and q, k, v and q_out apart from them and q_out from k, v and
+ * all of q but itself (else HS2_ERR_INVALID_ARG).
  * A page outside the cache writes no row.  Asynchronous; needs no workspace.
  */
 int hs2_rope_append(const hs2_tokens *q, const hs2_tokens *k, const hs2_tokens *v, const int32_t *positions,
@@ -341,7 +343,7 @@ size_t hs2_tree_attn_workspace(int32_t batch, int32_t tokens, int32_t num_kv_hea
  * draft order, at positions T_b - n_b .. T_b - 1.  Rows that a token does not see
  * do not reach its output, whatever they hold.
  *
- *   q, out     [B, N, Hq, d], apart from each other, N in [1, 64]; Hq / Hkv in {1, 2, 4, 8, 16, 32} (fp32: at most 8).
+ *   q, out     [B, N, Hq, d], apart from each other (parts of the same wider rows may be), N in [1, 64]; Hq / Hkv in {1, 2, 4, 8, 16, 32} (fp32: at most 8).
  *              Rows of tokens i >= n_b are not touched.
  *   num_draft  device int32 [B]: n_b, clamped to [0, min(N, T_b)]; NULL: N for all.
  *   tree_mask  device uint64 [B, N]; NULL: a chain (each token sees the earlier ones and itself).
@@ -363,8 +365,8 @@ int hs2_tree_attn(const hs2_tokens *q, const hs2_cache *k_cache, const hs2_cache
  *   path_len   device int32 [batch], clamped to [0, min(n_b, max_path)].
  *   num_draft  device int32 [batch]: n_b, as given to hs2_tree_attn(), clamped to [0, min(64, T_b)];
  *              NULL: max_path for all.
- *   lens_out   device int32 [batch], apart from seq_lens, num_draft and path_len.
- * The rows behind the new length are not defined.  Asynchronous; needs no workspace.
+ *   lens_out   device int32 [batch], apart from seq_lens, num_draft, path, path_len and page_table.
+ * The K and V caches lie apart (else HS2_ERR_INVALID_ARG).  The rows behind the new length are not defined.  Asynchronous; needs no workspace.
  */
 int hs2_tree_accept(const hs2_cache *k_cache, const hs2_cache *v_cache, const int32_t *seq_lens,
                     const int32_t *num_draft, const int32_t *path, const int32_t *path_len, int32_t batch,
@@ -413,9 +415,9 @@ int hs2_full_attn_accumulate_each(const hs2_heads *q, const hs2_cache *k_cache, 
  *   acc        as for hs2_full_attn_accumulate(); only positions below T_b are read.
  *   budget     >= 1; window in [0, budget].
  *   kept       device int32 [batch, Hkv, budget]: the kept positions, ascending, -1 behind the
- *              last (the call's own kernels read it back).
- *   lens_out   device int32 [batch], apart from seq_lens.
- * The rows and sums behind the new length are not defined.  Asynchronous; needs no workspace.
+ *              last (the call's own kernels read it back); apart from all other arguments.
+ *   lens_out   device int32 [batch], apart from seq_lens and page_table.
+ * The K and V caches lie apart (else HS2_ERR_INVALID_ARG).  The rows and sums behind the new length are not defined.  Asynchronous; needs no workspace.
  */
 int hs2_cache_evict(const hs2_cache *k_cache, const hs2_cache *v_cache, const int32_t *seq_lens, int32_t batch,
                     const int32_t *page_table, int32_t max_pages, float *acc, int64_t acc_stride, int32_t budget,

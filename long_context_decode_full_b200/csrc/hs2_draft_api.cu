@@ -3,6 +3,8 @@
 // launches.
 #include <math.h>
 
+#include <initializer_list>
+
 #include "hs2.h"
 #include "hs2_host.h"
 #include "hs2_internal.h"
@@ -58,10 +60,45 @@ TreePlan tree_plan(int B, int N, int G, int D, bool f32, bool small) {
 }
 
 bool same(const void *a, const void *b) { return a == b; }
-// two arrays of n int32
-bool overlap(const void *a, const void *b, int n) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b), bytes = (uintptr_t)n * 4;
-  return a && b && x < y + bytes && y < x + bytes;
+
+// Memory of an argument; NULL overlaps nothing.
+struct Span {
+  const void *data;
+  uint64_t bytes;
+};
+bool overlap(const Span &a, const Span &b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.data), y = reinterpret_cast<uintptr_t>(b.data);
+  return x && y && x < y + b.bytes && y < x + a.bytes;
+}
+bool overlap(const Span &a, std::initializer_list<Span> others) {
+  for (const Span &b : others)
+    if (overlap(a, b)) return true;
+  return false;
+}
+Span words(const void *data, int64_t n, int64_t per = 1) { return {data, (uint64_t)n * (uint64_t)per * 4}; }
+int elem_bytes(int dtype) { return dtype == HS2_F32 ? 4 : (dtype == HS2_BF16 ? 2 : 1); }
+Span rows_of(const hs2_cache *c) {
+  return {c->data, (uint64_t)c->num_slots * c->num_kv_heads * c->head_dim * elem_bytes(c->dtype)};
+}
+Span scales_of(const hs2_cache *c) { return words(c->scale, c->num_slots, c->num_kv_heads); }
+Span span(const hs2_tokens *x) {
+  return {x->data, ((uint64_t)((int64_t)x->batch * x->tokens - 1) * x->token_stride + (uint64_t)x->num_heads * x->head_dim) *
+                       elem_bytes(x->dtype)};
+}
+// Whether an element of a is one of b.  Parts of the same wider rows lie between each other without sharing one.
+bool overlap(const hs2_tokens *a, const hs2_tokens *b) {
+  if (!overlap(span(a), span(b))) return false;
+  if (a->token_stride != b->token_stride || a->dtype != b->dtype) return true;
+  const int64_t es = elem_bytes(a->dtype), row = a->token_stride * es;
+  int64_t off = (int64_t)((reinterpret_cast<intptr_t>(b->data) - reinterpret_cast<intptr_t>(a->data)) % row);
+  if (off < 0) off += row;
+  return off < (int64_t)a->num_heads * a->head_dim * es || off + (int64_t)b->num_heads * b->head_dim * es > row;
+}
+// K and V (and their scales) of a call that writes them
+int check_written(const hs2_cache *k, const hs2_cache *v) {
+  if (overlap(rows_of(k), rows_of(v)) || overlap(scales_of(k), scales_of(v)))
+    return fail(HS2_ERR_INVALID_ARG, "the K and V caches overlap");
+  return HS2_OK;
 }
 
 }  // namespace
@@ -137,6 +174,17 @@ int hs2_rope_append(const hs2_tokens *q, const hs2_tokens *k, const hs2_tokens *
     return fail(HS2_ERR_UNSUPPORTED, "rot_dim %d (a multiple of 16, at most head_dim %d)", rot_dim, k_cache->head_dim);
   int64_t t_cap;
   if ((rc = check_pages(k_cache, page_table, max_pages, k->batch, &t_cap))) return rc;
+  if ((rc = check_written(k_cache, v_cache))) return rc;
+  const Span caches[4] = {rows_of(k_cache), rows_of(v_cache), scales_of(k_cache), scales_of(v_cache)};
+  for (const Span &c : caches)
+    if (overlap(c, {span(k), span(v)}) || (q && overlap(c, span(q)))) return fail(HS2_ERR_INVALID_ARG, "q, k or v overlaps a cache");
+  if (q) {
+    hs2_tokens o = *q;
+    o.data = q_out;
+    o.token_stride = (int64_t)q->num_heads * q->head_dim;
+    if (overlap(span(&o), {caches[0], caches[1], caches[2], caches[3], span(k), span(v)}) || (!same(q_out, q->data) && overlap(&o, q)))
+      return fail(HS2_ERR_INVALID_ARG, "q_out overlaps q in part, or k, v or a cache");
+  }
   RopeParams p{};
   p.q = q ? q->data : nullptr;
   p.k = k->data;
@@ -219,6 +267,7 @@ int hs2_tree_attn(const hs2_tokens *q, const hs2_cache *k_cache, const hs2_cache
   if (reinterpret_cast<uintptr_t>(workspace) & 255) return fail(HS2_ERR_WORKSPACE, "workspace not 256-byte aligned");
   if (workspace_bytes < plan.total)
     return fail(HS2_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, plan.total);
+  if (overlap(q, out)) return fail(HS2_ERR_INVALID_ARG, "out overlaps q");
   uint8_t *w = static_cast<uint8_t *>(workspace);
   TreeParams p{};
   p.q = q->data;
@@ -281,8 +330,10 @@ int hs2_tree_accept(const hs2_cache *k_cache, const hs2_cache *v_cache, const in
   if (max_path < 1 || max_path > kMaxDraft) return fail(HS2_ERR_UNSUPPORTED, "max_path %d out of [1, %d]", max_path, kMaxDraft);
   AcceptParams p{};
   if ((rc = check_pages(k_cache, page_table, max_pages, batch, &p.t_cap))) return rc;
-  if (overlap(lens_out, seq_lens, batch) || overlap(lens_out, num_draft, batch) || overlap(lens_out, path_len, batch))
-    return fail(HS2_ERR_INVALID_ARG, "lens_out overlaps seq_lens, num_draft or path_len");
+  if (overlap(words(lens_out, batch), {words(seq_lens, batch), words(num_draft, batch), words(path_len, batch),
+                                       words(path, batch, max_path), words(page_table, batch, max_pages)}))
+    return fail(HS2_ERR_INVALID_ARG, "lens_out overlaps seq_lens, num_draft, path, path_len or page_table");
+  if ((rc = check_written(k_cache, v_cache))) return rc;
   p.k = const_cast<void *>(k_cache->data);
   p.v = const_cast<void *>(v_cache->data);
   p.k_scale = const_cast<float *>(k_cache->scale);
@@ -296,7 +347,7 @@ int hs2_tree_accept(const hs2_cache *k_cache, const hs2_cache *v_cache, const in
   p.B = batch;
   p.M = max_path;
   p.Hkv = k_cache->num_kv_heads;
-  p.row_bytes = p.Hkv * k_cache->head_dim * (k_cache->dtype == HS2_F32 ? 4 : (k_cache->dtype == HS2_BF16 ? 2 : 1));
+  p.row_bytes = p.Hkv * k_cache->head_dim * elem_bytes(k_cache->dtype);
   p.page_size = k_cache->page_size;
   p.max_pages = max_pages;
   p.num_slots = k_cache->num_slots;
@@ -315,9 +366,15 @@ int hs2_cache_evict(const hs2_cache *k_cache, const hs2_cache *v_cache, const in
   if (reinterpret_cast<uintptr_t>(acc) & 3) return fail(HS2_ERR_INVALID_ARG, "acc is misaligned");
   EvictParams p{};
   if ((rc = check_pages(k_cache, page_table, max_pages, batch, &p.t_cap))) return rc;
-  if (overlap(lens_out, seq_lens, batch)) return fail(HS2_ERR_INVALID_ARG, "lens_out overlaps seq_lens");
+  if (overlap(words(lens_out, batch), {words(seq_lens, batch), words(page_table, batch, max_pages)}))
+    return fail(HS2_ERR_INVALID_ARG, "lens_out overlaps seq_lens or page_table");
   if (acc_stride < p.t_cap)
     return fail(HS2_ERR_INVALID_ARG, "acc_stride %lld < capacity %lld", (long long)acc_stride, (long long)p.t_cap);
+  const int64_t units = (int64_t)batch * k_cache->num_kv_heads;
+  if (overlap(words(kept, units, budget), {words(seq_lens, batch), words(page_table, batch, max_pages), words(lens_out, batch),
+                                           words(acc, units, acc_stride)}))
+    return fail(HS2_ERR_INVALID_ARG, "kept overlaps seq_lens, page_table, lens_out or acc");
+  if ((rc = check_written(k_cache, v_cache))) return rc;
   p.k = const_cast<void *>(k_cache->data);
   p.v = const_cast<void *>(v_cache->data);
   p.k_scale = const_cast<float *>(k_cache->scale);
@@ -332,7 +389,7 @@ int hs2_cache_evict(const hs2_cache *k_cache, const hs2_cache *v_cache, const in
   p.Hkv = k_cache->num_kv_heads;
   p.budget = budget;
   p.window = window;
-  p.head_bytes = k_cache->head_dim * (k_cache->dtype == HS2_F32 ? 4 : (k_cache->dtype == HS2_BF16 ? 2 : 1));
+  p.head_bytes = k_cache->head_dim * elem_bytes(k_cache->dtype);
   p.page_size = k_cache->page_size;
   p.max_pages = max_pages;
   p.num_slots = k_cache->num_slots;

@@ -138,6 +138,34 @@ def test_tree_attn_short_drafts_in_a_long_drafts_workspace(dtype, hkv, G, d, N):
         check(out, want, bound, ~want.isnan())
 
 
+# ---------------------------------------------------------------- parts of the same rows
+def test_tree_attn_queries_and_output_side_by_side():
+    """q and out as parts of the same wider rows, in either order: between each other in memory, no element shared."""
+    for at_q, at_o in ((0, 8), (9, 0)):
+        c, q, masks, words = tree_case("bf16", 2, 4, 128, 64, 6, [300, 7], [6, 6], seed=2)
+        wide = torch.full((2, 6, 17, 128), 77.0, device="cuda", dtype=q.dtype)
+        wide[:, :, at_q:at_q + 8] = q
+        before = wide.clone()
+        out = hs2.tree_attn(wide[:, :, at_q:at_q + 8], c.k, c.v, c.lens, tree_mask=words, out=wide[:, :, at_o:at_o + 8], **c.kw())
+        want, bound = R.tree_reference(c, q, [6, 6], masks, "bf16")
+        check(out, want, bound, ~want.isnan())
+        wide[:, :, at_o:at_o + 8] = before[:, :, at_o:at_o + 8]
+        assert torch.equal(wide, before)
+
+
+def test_rope_append_queries_in_place_beside_keys_and_values():
+    """One token per sequence of a fused projection, its queries rotated where they are."""
+    c = R.PagedCache("bf16", [40], 2, 128, 16, seed=1)
+    qkv = torch.randn(1, 1, 12, 128, device="cuda", generator=gen(7)).bfloat16()
+    pos, table, before = i32([[39]]), hs2.rope_table(128), c.snapshot()
+    want = hs2.rope_append(qkv[:, :, :8].contiguous(), qkv[:, :, 8:10], qkv[:, :, 10:], pos, table, c.k, c.v, c.lens, **c.kw())
+    rows = c.k[c.slots(0, 39)].clone()
+    c.k.copy_(before[0])
+    same = qkv.clone()
+    got = hs2.rope_append(same[:, :, :8], same[:, :, 8:10], same[:, :, 10:], pos, table, c.k, c.v, c.lens, q_out=same[:, :, :8], **c.kw())
+    assert torch.equal(got, want) and torch.equal(same[:, :, 8:], qkv[:, :, 8:]) and torch.equal(c.k[c.slots(0, 39)], rows)
+
+
 # ---------------------------------------------------------------- accepted paths
 @pytest.mark.parametrize("dtype,width", [("bf16", 5), ("e4m3", 1), ("f32", 17)])
 def test_tree_accept_path_narrower_than_the_draft(dtype, width):
