@@ -535,10 +535,13 @@ def rope_append(q, k_new, v_new, positions, table: RopeTable, k, v, seq_lens, pa
 
 
 def tree_mask(parents) -> torch.Tensor:
-    """int64 [B, N] masks for tree_attn() from parents [B, N] (CPU): parents[b, i] < i is the draft that token i
+    """int64 [B, N] masks for tree_attn() from parents [B, N] (CPU), N <= 64: parents[b, i] < i is the draft that token i
     continues, -1 for the context; each token sees its ancestors and itself."""
+    parents = torch.as_tensor(parents)
+    if parents.dim() != 2 or parents.shape[1] > 64:
+        raise HS2Error(ERR_UNSUPPORTED, f"parents: shape {tuple(parents.shape)}, expected [B, N] with N of at most 64")
     rows = []
-    for row in torch.as_tensor(parents).tolist():
+    for row in parents.tolist():
         m = []
         for i, p in enumerate(row):
             if not -1 <= p < i:

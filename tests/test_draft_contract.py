@@ -101,3 +101,10 @@ def test_tree_accept_refuses_lengths_on_its_inputs(libhs2, out):
 def test_cache_evict_refuses_results_on_its_inputs(libhs2, kw, word):
     at = dict(dict(kept=A[7], out=A[8]), **kw)
     refused(abi.evict(lens=A[5], acc=A[6], pt=A[9], **at, **two_caches()), word)
+
+
+# ---------------------------------------------------------------- masks
+@pytest.mark.parametrize("shape", [(1, 65), (2, 200), (3,), (1, 2, 2)])
+def test_tree_mask_refuses_drafts_that_its_words_cannot_hold(shape):
+    with pytest.raises(hs2.HS2Error):
+        hs2.tree_mask(torch.full(shape, -1))
