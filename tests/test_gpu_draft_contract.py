@@ -166,6 +166,41 @@ def test_rope_append_queries_in_place_beside_keys_and_values():
     assert torch.equal(got, want) and torch.equal(same[:, :, 8:], qkv[:, :, 8:]) and torch.equal(c.k[c.slots(0, 39)], rows)
 
 
+# ---------------------------------------------------------------- rows that see nothing, drafts that nobody may see
+@pytest.mark.parametrize("dtype,N,G,d,T", [
+    ("f32", 4, 2, 128, 200), ("f32", 8, 1, 64, 3000),    # one block of 8 rows
+    ("f32", 4, 4, 64, 200), ("f32", 8, 2, 128, 3000),    # two
+    ("f32", 8, 4, 128, 300), ("f32", 8, 4, 64, 3000),    # 32 rows, in tiles of 32 and of 64 positions
+    ("f32", 7, 8, 128, 300),                             # 64 rows
+    ("bf16", 8, 8, 128, 300), ("bf16", 4, 4, 64, 300), ("e4m3", 8, 8, 128, 300), ("e4m3", 5, 2, 128, 3000)])
+def test_tree_attn_small_trees_with_empty_rows_and_poisoned_drafts(dtype, N, G, d, T):
+    """Every shape of the kernels: masks that leave rows empty, with and without a context, and drafts whose values or
+    keys are infinite or NaN, seen by themselves alone."""
+    lens = [N, N, T]
+    mask = [0 if i % 5 == 0 else 1 << i if i in (2, 3) else 1 << i | 1 << 1 for i in range(N)]
+    masks = [mask, [m | ~((1 << N) - 1) & (1 << 64) - 1 for m in mask], mask]  # bits behind the draft mean nothing
+    c, q, masks, words = tree_case(dtype, 2, G, d, 16, N, lens, [N] * 3, seed=9, masks=masks)
+    for b in range(3):
+        values, keys = (int(s) for s in c.slots(b, [lens[b] - N + 2, lens[b] - N + 3]))
+        if dtype == "e4m3":
+            c.v.view(torch.uint8)[values, :, 5] = 0x7f
+            c.k.view(torch.uint8)[keys, :, 100] = 0xff
+        else:
+            c.v[values, :, 5] = NAN
+            c.v[values, :, 9] = -math.inf
+            c.k[keys, :, 60] = NAN
+    clean = R.PagedCache(dtype, lens, 2, d, 16, 9)
+    want, bound = R.tree_reference(clean, q, [N] * 3, masks, dtype)
+    out = torch.full_like(q, 77.0)
+    hs2.tree_attn(q, c.k, c.v, c.lens, tree_mask=words, out=out, **c.kw())
+    good = torch.tensor([i not in (2, 3) for i in range(N)], device="cuda")
+    assert bool(((out.double() - want).abs() <= bound)[:, good].all())
+    assert bool((out[:2, [i % 5 == 0 for i in range(N)]] == 0).all())
+    assert bool(out[:, 2, :, 5].isnan().all()) and bool(out[:, 2, :, :5].isfinite().all()) and bool(out[:, 2, :, 10:].isfinite().all())
+    assert dtype == "e4m3" or bool((out[:, 2, :, 9] == -math.inf).all())
+    assert bool(out[:, 3].isnan().all())
+
+
 # ---------------------------------------------------------------- accepted paths
 @pytest.mark.parametrize("dtype,width", [("bf16", 5), ("e4m3", 1), ("f32", 17)])
 def test_tree_accept_path_narrower_than_the_draft(dtype, width):
