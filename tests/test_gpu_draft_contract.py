@@ -261,6 +261,38 @@ def test_accumulate_starts_each_sequences_own_new_tokens(dtype, G, page):
             assert torch.equal(R.bits(acc[b, h, T:]), R.bits(acc0[b, h, T:]))
 
 
+# ---------------------------------------------------------------- the full layer's output beside its sums
+@pytest.mark.parametrize("dtype,hkv,G,d,page", [
+    ("bf16", 2, 8, 128, 64), ("bf16", 1, 32, 64, 16), ("bf16", 1, 1, 128, 0), ("e4m3", 1, 16, 128, 32), ("e4m3", 2, 8, 128, 64),
+    ("f32", 2, 1, 64, 0), ("f32", 1, 8, 128, 16), ("f32", 3, 2, 128, 48), ("f32", 1, 4, 64, 64)])
+def test_full_attn_accumulate_output_within_its_bound(dtype, hkv, G, d, page):
+    """Elementwise, so that a segment left out or weighted wrongly shows: the oracle without a sixteenth of the positions
+    must not pass (a quarter of the longest: outputs shrink with the root of the length, bounds do not).
+
+    R.attend()'s bound holds for the full layer's kernels, but that weights over E4M3 are rounded to fp16: 2^-11 instead
+    of 2^-8, and, normalised by the largest V scale so far, below 2^-14 by up to 2^-25 of it, times the row's code, where
+    the sum of weights is at least 1."""
+    lens = [1, 700, 0, 130, 4099, 20011]
+    c = R.PagedCache(dtype, lens, hkv, d, page, seed=17)
+    q = torch.randn(len(lens), hkv * G, d, device="cuda", generator=gen(18)).to(R.q_dtype(dtype))
+    acc = torch.zeros(len(lens), hkv, c.cap, device="cuda")
+    out, _ = hs2.full_attn_accumulate(q, c.k, c.v, c.lens, acc, **c.kw())
+    for b, T in enumerate(lens):
+        k, v = c.wide("k", b, torch.arange(T)), c.wide("v", b, torch.arange(T))
+        seen = torch.ones(G, T, dtype=torch.bool, device="cuda")
+        for h in range(hkv):
+            rows, got = q[b, h * G:(h + 1) * G].double(), out[b, h * G:(h + 1) * G].double()
+            want, bound, p = R.attend(rows, k[:, h], v[:, h], seen, dtype)
+            if dtype == "e4m3" and T:
+                s = c.slots(b, torch.arange(T))
+                bound = bound - (2.0 ** -8 - 2.0 ** -11) * (p @ v[:, h].abs()) + 2.0 ** -25 * c.v_scale[s, h].max().double() * c.v[s, h].double().abs().sum(0)
+            assert bool(((got - want).abs() <= bound).all()), (b, h, float(((got - want).abs() - bound).max()))
+            if T >= 130:
+                cut = T // 16 if T < 5000 else T // 4
+                short, _, _ = R.attend(rows, k[cut:, h], v[cut:, h], seen[:, cut:], dtype)
+                assert bool(((short - want).abs() > bound).any())
+
+
 # ---------------------------------------------------------------- together
 @pytest.mark.parametrize("dtype,page", [("bf16", 16), ("e4m3", 64), ("f32", 0)])
 def test_verify_accumulate_evict_reads_no_undefined_sum(dtype, page):
