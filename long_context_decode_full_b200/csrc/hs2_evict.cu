@@ -478,8 +478,11 @@ cudaError_t launch_evict(const EvictParams &p0, bool scales, int sms, cudaStream
   e = p.t_cap <= 512 * kPickKeys ? launch_ex(pick_kernel<512>, dim3((unsigned)(units * C)), dim3(512), 0, s, C, p)
                                  : launch_ex(pick_kernel<1024>, dim3((unsigned)(units * C)), dim3(1024), 0, s, C, p);
   if (e != cudaSuccess) return e;
-  // CTAs per unit and job: no more than fit beside each other (two per SM), and a
-  // run of theirs (at least 32 rows each) no longer than the budget
+  // CTAs per unit and job: no more for K's and V's rows than fit beside each other (two
+  // per SM), and a run of theirs (at least 32 rows each) no longer than the budget.  The
+  // jobs of the sums and scales come behind in the grid and take places that are left or
+  // become free, in rings of the rows' size: 24 sequences of 4 heads in E4M3 launch 480 CTAs
+  // on 296 places.
   C = 1;
   const int jobs = scales ? 5 : 3;
   while (C < 8 && (int64_t)units * 2 * C * 2 <= 2 * sms && p.budget > C * 64) C *= 2;
@@ -487,7 +490,7 @@ cudaError_t launch_evict(const EvictParams &p0, bool scales, int sms, cudaStream
     const cudaError_t err = set_smem_once(reinterpret_cast<const void *>(kern), (int)bytes);
     return err != cudaSuccess ? err : launch_ex(kern, dim3((unsigned)(units * C), jobs), dim3(kMoveThreads), bytes, s, C, p);
   };
-  // Where one CTA per SM is enough, twice the rows per step: a step takes 1.2 us whatever it moves.
+  // Where one CTA per SM is enough for K and V, twice the rows per step: a step takes 1.2 us whatever it moves.
   if ((int64_t)units * 2 * C <= sms) return move(move_kernel<8>, sizeof(MoveRing<8>));
   return move(move_kernel<4>, sizeof(MoveRing<4>));
 }

@@ -11,10 +11,13 @@
 // in registers (half the rows where a unit has at most 32, and half the positions
 // where the tiles would not fill the GPU; at most 16 rows have a kernel of their own,
 // below); Q, K, V and the weights are in shared memory, K's and Q's rows
-// padded by 16 bytes so that 16-byte reads of 8 rows meet 32 banks.  Bound by the
-// FMA units on long caches, by latency on short ones: 5 drafts x 4 heads over 2,048
-// tokens take 14.8 us with the joining kernel (64-row, 64-position shapes and shares
-// without tiles: 53 us).
+// padded by 16 bytes so that 16-byte reads of 8 rows meet 32 banks.  Bound by
+// latency on short caches: 5 drafts x 4 heads over 2,048 tokens take 14.8 us with the
+// joining kernel (64-row, 64-position shapes and shares without tiles: 53 us).  Long
+// ones run at 20 to 22 TFLOP/s, 0.3 of what the FMA units could (every 16-byte read of
+// shared memory feeds 8 of their operations, and one tile's loads, logits and product
+// wait for one another): 64 x 8 rows over 2 x 16,384 tokens 1.55 ms, 8 x 8 rows over
+// 8 x 20,000 0.94 ms, 4 x 8 rows of the same 0.51 ms (4 KV heads, d 128).
 #include <type_traits>
 
 #include "hs2.h"

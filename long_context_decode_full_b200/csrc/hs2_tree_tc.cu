@@ -28,6 +28,15 @@
 // The key's scale multiplies the logit.  V's codes are converted to bf16 (exact)
 // by a warpgroup of its own, and its scale joins the weight before it is rounded.
 //
+// Weights are rounded to bf16 for the product with V (2^-8 at most of each; their
+// sum l takes them unrounded), which with the output's own rounding leaves 0.0024 of
+// an output's size where exact weights leave 0.0017 (random rows).  Over a bf16
+// cache the product has no other type for them.  Over E4M3 fp16 would hold three more
+// bits, as the decode step's kernels do, but only of weights times scales within
+// 2^-14 of the largest, and nothing below 2^-24: a million rows 2^-30 below one that
+// dominates (a first row without a value of its own) would be lost, where bf16 keeps
+// them as exact as any.
+//
 // Roles: warps 0-3 and 4-7 the streams, 8-11 the values (conversion, and rows
 // that must not be multiplied, below), 12 the TMA loads, 13 the MMA issue, 14-15
 // E4M3's scales.  Register shares follow the roles.

@@ -201,6 +201,33 @@ def test_tree_attn_small_trees_with_empty_rows_and_poisoned_drafts(dtype, N, G, 
     assert bool(out[:, 3].isnan().all())
 
 
+# ---------------------------------------------------------------- weights far below a dominating one
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3", "f32"])
+@pytest.mark.parametrize("at", [3, 30000])
+def test_tree_attn_weights_far_below_a_dominating_one(dtype, at):
+    """One row takes all but 2^-20 of the weight and has no value, as the first row of a context often does: the output is
+    what the 40,000 others add, with weights 2^-40 below the largest, and as exact as any."""
+    T, N, hkv, G, d = 40000, 5, 1, 4, 128
+    c, q, masks, words = tree_case(dtype, hkv, G, d, 64, N, [T], [N], seed=23)
+    q[..., 0] = 8.0
+    row = int(c.slots(0, at))
+    if dtype == "e4m3":
+        live = c.slots(0, torch.arange(T))
+        c.k.view(torch.uint8)[live, :, 0] = 0
+        c.k.view(torch.uint8)[row], c.v.view(torch.uint8)[row] = 0, 0
+        c.k[row, :, 0] = 448.0
+        c.k_scale[row] = 39.0 / 448.0
+    else:
+        c.k[c.slots(0, torch.arange(T)), :, 0] = 0.0
+        c.k[row], c.v[row] = 0.0, 0.0
+        c.k[row, :, 0] = 39.0
+    out = torch.full_like(q, 77.0)
+    hs2.tree_attn(q, c.k, c.v, c.lens, tree_mask=words, out=out, **c.kw())
+    want, bound = R.tree_reference(c, q, [N], masks, dtype)
+    assert float(want.abs().max()) < 2.0 ** -20
+    check(out, want, bound, ~want.isnan())
+
+
 # ---------------------------------------------------------------- accepted paths
 @pytest.mark.parametrize("dtype,width", [("bf16", 5), ("e4m3", 1), ("f32", 17)])
 def test_tree_accept_path_narrower_than_the_draft(dtype, width):
