@@ -433,3 +433,170 @@ def test_rope_append_e4m3_codes_are_the_quotients():
     for b in range(B):
         s = c.slots(b, torch.arange(N))
         assert torch.equal(c.v_scale[s], scale[b]) and torch.equal(R.bits(c.v[s]), R.bits(codes[b]))
+
+
+# ---------------------------------------------------------------- sizes at both ends
+def all_calls(c, N, lens, G, d, hkv, acc, dtype, seed):
+    """Every call of a verification step on cache c; returns what they gave."""
+    B = len(lens)
+    qkv = torch.randn(B, N, hkv * (G + 2), d, device="cuda", generator=gen(seed)).to(R.q_dtype(dtype))
+    pos = torch.arange(N, device="cuda", dtype=torch.int32).repeat(B, 1) + c.lens[:, None] - N
+    q = hs2.rope_append(qkv[:, :, :hkv * G], qkv[:, :, hkv * G:hkv * (G + 1)], qkv[:, :, hkv * (G + 1):], pos, hs2.rope_table(64),
+                        c.k, c.v, c.lens, **c.kw())
+    out = hs2.tree_attn(q, c.k, c.v, c.lens, **c.kw())
+    path = torch.tensor([[1, N - 1]] * B, dtype=torch.int32, device="cuda")
+    two = torch.full((B,), 2, dtype=torch.int32, device="cuda")
+    lens = hs2.tree_accept(c.k, c.v, c.lens, path, two, num_draft=two * 0 + N, **c.kw())
+    o, _ = hs2.full_attn_accumulate(q[:, 1].contiguous(), c.k, c.v, lens, acc, fresh=two, **c.kw())
+    lens2, kept = hs2.cache_evict(c.k, c.v, lens, acc, 100, **c.kw())
+    return [q, out, lens, o, lens2, kept, acc]
+
+
+@pytest.mark.parametrize("dtype,elements", [("bf16", 2 ** 32), ("e4m3", 2 ** 32), ("f32", 2 ** 31)])
+def test_calls_at_the_end_of_a_large_cache(dtype, elements):
+    """Rows whose elements lie beyond 32 bits: the same results as in a small cache."""
+    hkv, G, d, N, page, lens = 8, 2, 128, 4, 64, [300, 70, 129]
+    small = R.PagedCache(dtype, lens, hkv, d, page, seed=33, poison=False)
+    acc = torch.rand(len(lens), hkv, small.cap, device="cuda", generator=gen(34))
+    n = small.k.shape[0]
+    slots = (elements // (hkv * d) // page + 1) * page + n
+    big = R.PagedCache(dtype, lens, hkv, d, page, seed=33, poison=False)
+    for name in ("k", "v", "k_scale", "v_scale"):
+        x = getattr(small, name)
+        if x is not None:
+            y = torch.empty((slots,) + tuple(x.shape[1:]), dtype=x.dtype, device="cuda")
+            y[-n:] = x
+            setattr(big, name, y)
+    big.table = small.table + (slots - n) // page
+    got = all_calls(big, N, lens, G, d, hkv, acc.clone(), dtype, 35)
+    want = all_calls(small, N, lens, G, d, hkv, acc.clone(), dtype, 35)
+    for x, y in zip(got, want):
+        assert torch.equal(R.bits(x), R.bits(y))
+    for name in ("k", "v", "k_scale", "v_scale"):
+        x = getattr(small, name)
+        assert x is None or torch.equal(R.bits(getattr(big, name)[-n:]), R.bits(x))
+
+
+@pytest.mark.parametrize("dtype,G,N", [("bf16", 2, 3), ("e4m3", 1, 2), ("f32", 2, 2), ("f32", 8, 5)])
+def test_calls_of_a_thousand_sequences(dtype, G, N):
+    """More sequences than a warp or a block walks at once, a few tokens each, some without any."""
+    hkv, d, B = 1, 128, 1100
+    lens = [(7 * i) % 23 for i in range(B)]
+    c, q, masks, words = tree_case(dtype, hkv, G, d, 16, N, lens, [N] * B, seed=36)
+    out = torch.full_like(q, 77.0)
+    hs2.tree_attn(q, c.k, c.v, c.lens, tree_mask=words, out=out, **c.kw())
+    want, bound = R.tree_reference(c, q, [N] * B, masks, dtype)
+    check(out, want, bound, ~want.isnan())
+    acc = torch.full((B, hkv, c.cap), NAN, device="cuda")
+    hs2.full_attn_accumulate(q[:, 0].contiguous(), c.k, c.v, c.lens, acc, fresh=c.lens, **c.kw())
+    sums = acc.clone()
+    for b in range(0, B, 41):
+        if lens[b]:
+            w, slack = weights(c, q[:, 0], b, 0, G, d)
+            assert bool(((acc[b, 0, :lens[b]].double() - w).abs() <= slack * w).all())
+    before = c.snapshot()
+    lens_out, kept = hs2.cache_evict(c.k, c.v, c.lens, acc, 9, 2, **c.kw())
+    assert lens_out.tolist() == [min(t, 9) for t in lens]
+    for b in range(B):
+        keep = R.kept_positions(sums[b, 0, :lens[b]].tolist(), lens[b], 9, 2)
+        assert kept[b, 0].tolist() == keep + [-1] * (9 - len(keep))
+        assert torch.equal(R.bits(c.v[c.slots(b, list(range(len(keep))))]), R.bits(before[1][c.slots(b, keep)]))
+
+
+def test_tree_attn_chain_of_64():
+    """The default mask at its widest, in each type."""
+    for dtype in ("bf16", "e4m3", "f32"):
+        c, q, _, _ = tree_case(dtype, 1, 4, 128, 64, 64, [64, 500], [64, 64], seed=37)
+        out = torch.full_like(q, 77.0)
+        hs2.tree_attn(q, c.k, c.v, c.lens, out=out, **c.kw())
+        want, bound = R.tree_reference(c, q, [64, 64], [[(1 << i + 1) - 1 for i in range(64)]] * 2, dtype)
+        check(out, want, bound, ~want.isnan())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3", "f32"])
+def test_tree_attn_queries_of_zero_and_of_all_sizes(dtype):
+    """Rows of zeros see the mean of the values; tiny and large rows beside them."""
+    c, q, masks, words = tree_case(dtype, 2, 4, 128, 64, 8, [700, 20], [8, 8], seed=38)
+    q *= torch.tensor([0.0, 1e-38, 1e-30, 1e-3, 1.0, 3.0, 10.0, 30.0], device="cuda", dtype=q.dtype).view(1, 8, 1, 1)
+    out = torch.full_like(q, 77.0)
+    hs2.tree_attn(q, c.k, c.v, c.lens, tree_mask=words, out=out, **c.kw())
+    want, bound = R.tree_reference(c, q, [8, 8], masks, dtype)
+    check(out, want, bound, ~want.isnan())
+
+
+# ---------------------------------------------------------------- pages outside the cache
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3", "f32"])
+def test_moves_between_pages_outside_the_cache_move_nothing(dtype):
+    """accept and evict with page numbers that the cache does not have: rows whose two places exist move, no other row
+    changes."""
+    lens, hkv, page, n, budget = [100, 90], 2, 16, 40, 50
+    for call in ("accept", "evict"):
+        c = R.PagedCache(dtype, lens, hkv, 128, page, seed=39, poison=False)
+        good = c.table.clone()
+        bad = [(0, 1, 2 ** 31 - 1), (0, 4, -3), (1, 0, c.k.shape[0] // page), (1, 5, -2 ** 31)]
+        table = good.clone()
+        for b, j, number in bad:
+            table[b, j] = number
+        exists = lambda b, t: all((b, t // page) != x[:2] for x in bad)  # noqa: B023, E731
+        before = c.snapshot()
+        kw = dict(c.kw(), page_table=table)
+        moves = []
+        if call == "accept":
+            path = torch.arange(n - 1, -1, -2).repeat(2, 1)
+            hs2.tree_accept(c.k, c.v, c.lens, path.to(torch.int32).cuda(), i32([20, 20]), num_draft=i32([n, n]), **kw)
+            moves = [(b, T - n + int(path[b, i]), T - n + i, range(hkv)) for b, T in enumerate(lens) for i in range(20)]
+        else:
+            acc = torch.rand(2, hkv, c.cap, device="cuda", generator=gen(40))
+            _, kept = hs2.cache_evict(c.k, c.v, c.lens, acc, budget, 10, **kw)
+            moves = [(b, t, i, [h]) for b in range(2) for h in range(hkv) for i, t in enumerate(kept[b, h].tolist())]
+        want = [None if x is None else x.clone() for x in before]
+        for b, src, dst, heads in moves:
+            if exists(b, src) and exists(b, dst):
+                s, t = int(c.slots(b, src)), int(c.slots(b, dst))
+                for x, y in zip(want, before):
+                    if x is not None:
+                        for h in heads:
+                            x[t, h] = y[s, h]
+        for x, y in zip((c.k, c.v, c.k_scale, c.v_scale), want):
+            assert x is None or torch.equal(R.bits(x), R.bits(y)), call
+
+
+# ---------------------------------------------------------------- captured
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3", "f32"])
+def test_counts_are_read_at_every_replay(dtype):
+    """Path widths, drafts' sizes and each sequence's new positions in a graph: other counts at every replay."""
+    hkv, G, d, N, B = 2, 4, 128, 16, 3
+    lens = [300, 60, 129]
+    q = torch.randn(B, hkv * G, d, device="cuda", generator=gen(41)).to(R.q_dtype(dtype))
+    cases = [R.PagedCache(dtype, lens, hkv, d, 16, seed=42, poison=False) for _ in (0, 1)]
+    acc0 = torch.rand(B, hkv, cases[0].cap, device="cuda", generator=gen(43))
+    ws = hs2.alloc_workspace(B, hkv, G, d, cases[0].cap)
+    args = [dict(path=i32([[2, 5, 9]] * B), plen=i32([3] * B), nd=i32([N] * B), acc=acc0.clone(), lens=torch.zeros_like(c.lens),
+                 out=torch.zeros_like(q)) for c in cases]
+
+    def step(c, a):
+        hs2.tree_accept(c.k, c.v, c.lens, a["path"], a["plen"], num_draft=a["nd"], lens_out=a["lens"], **c.kw())
+        hs2.full_attn_accumulate(q, c.k, c.v, a["lens"], a["acc"], fresh=a["plen"], out=a["out"], workspace=ws, **c.kw())
+
+    start = cases[0].snapshot()
+    step(cases[0], args[0])
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(cases[0], args[0])
+    for path, plen, nd in (([[0, 1, 2], [3, 1, 15], [4, 4, 4]], [1, 3, 0], [16, 16, 5]), ([[7, 8, 9]] * 3, [0, 2, 9], [10, 9, 16])):
+        for c, a in zip(cases, args):
+            for x, y in zip((c.k, c.v, c.k_scale, c.v_scale), start):
+                if x is not None:
+                    x.copy_(y)
+            a["path"].copy_(i32(path))
+            a["plen"].copy_(i32(plen))
+            a["nd"].copy_(i32(nd))
+            a["acc"].copy_(acc0)
+        g.replay()
+        step(cases[1], args[1])
+        torch.cuda.synchronize()
+        for x, y in zip(cases[0].tensors() + list(args[0].values()), cases[1].tensors() + list(args[1].values())):
+            assert torch.equal(R.bits(x), R.bits(y))
+        a = [max(0, min(p, 3, n)) for p, n in zip(plen, nd)]
+        assert args[0]["lens"].tolist() == [t - n + p for t, n, p in zip(lens, nd, a)]
