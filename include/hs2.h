@@ -341,7 +341,9 @@ size_t hs2_tree_attn_workspace(int32_t batch, int32_t tokens, int32_t num_kv_hea
  *     out[b, i, h] = softmax(q k^T / sqrt(d)) v   over what it sees,
  * zeros when it sees nothing.  The drafts' K/V rows are already in the cache, in
  * draft order, at positions T_b - n_b .. T_b - 1.  Rows that a token does not see
- * do not reach its output, whatever they hold.
+ * do not reach its output, whatever they hold.  Over bf16 and E4M3 caches values are
+ * summed with weights of up to 2^15 before they are normalised: finite values below
+ * 2^90 in magnitude cannot overflow.
  *
  *   q, out     [B, N, Hq, d], apart from each other (parts of the same wider rows may be), N in [1, 64]; Hq / Hkv in {1, 2, 4, 8, 16, 32} (fp32: at most 8).
  *              Rows of tokens i >= n_b are not touched.
