@@ -257,6 +257,9 @@ int hs2_sparse_attn(const hs2_heads *q_l, const hs2_cache *k_cache, const hs2_ca
  * paged caches under the same conventions; a page belongs to one sequence.
  * Where rows move, a key keeps the rotation of the position it was written
  * for, so positions are given apart from lengths.
+ * The calls that write the caches want K and V apart from each other: memory of their own, or
+ * pages of one pool, K's and V's whole pages from each other (v_cache.data a number of pages
+ * behind k_cache.data, with page numbers that keep them apart); else HS2_ERR_INVALID_ARG.
  * ---------------------------------------------------------------------------
  */
 
@@ -319,8 +322,8 @@ int hs2_rope_table(const hs2_rope *rope, uint64_t *table, float *rot_scale);
  *   num_new    device int32 [B]: n_b, clamped to [0, min(N, T_b)]; NULL: N for all.
  *   q_out      device [B, N, Hq, d], contiguous, dtype of q; may be q->data when q is
  *              contiguous.  Rows of tokens i >= n_b are not touched.
- * The K and V caches lie apart, and q, k, v and q_out apart from them and q_out from k, v and
- * all of q but itself (else HS2_ERR_INVALID_ARG).
+ * q_out lies apart from k, v and every part of q but q itself (else HS2_ERR_INVALID_ARG); no row
+ * that is written is read by the call.
  * A page outside the cache writes no row.  Asynchronous; needs no workspace.
  */
 int hs2_rope_append(const hs2_tokens *q, const hs2_tokens *k, const hs2_tokens *v, const int32_t *positions,
@@ -368,7 +371,7 @@ int hs2_tree_attn(const hs2_tokens *q, const hs2_cache *k_cache, const hs2_cache
  *   num_draft  device int32 [batch]: n_b, as given to hs2_tree_attn(), clamped to [0, min(64, T_b)];
  *              NULL: max_path for all.
  *   lens_out   device int32 [batch], apart from seq_lens, num_draft, path, path_len and page_table.
- * The K and V caches lie apart (else HS2_ERR_INVALID_ARG).  The rows behind the new length are not defined.  Asynchronous; needs no workspace.
+ * The rows behind the new length are not defined.  Asynchronous; needs no workspace.
  */
 int hs2_tree_accept(const hs2_cache *k_cache, const hs2_cache *v_cache, const int32_t *seq_lens,
                     const int32_t *num_draft, const int32_t *path, const int32_t *path_len, int32_t batch,
@@ -419,7 +422,7 @@ int hs2_full_attn_accumulate_each(const hs2_heads *q, const hs2_cache *k_cache, 
  *   kept       device int32 [batch, Hkv, budget]: the kept positions, ascending, -1 behind the
  *              last (the call's own kernels read it back); apart from all other arguments.
  *   lens_out   device int32 [batch], apart from seq_lens and page_table.
- * The K and V caches lie apart (else HS2_ERR_INVALID_ARG).  The rows and sums behind the new length are not defined.  Asynchronous; needs no workspace.
+ * The rows and sums behind the new length are not defined.  Asynchronous; needs no workspace.
  */
 int hs2_cache_evict(const hs2_cache *k_cache, const hs2_cache *v_cache, const int32_t *seq_lens, int32_t batch,
                     const int32_t *page_table, int32_t max_pages, float *acc, int64_t acc_stride, int32_t budget,

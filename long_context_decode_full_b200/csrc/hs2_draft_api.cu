@@ -77,10 +77,6 @@ bool overlap(const Span &a, std::initializer_list<Span> others) {
 }
 Span words(const void *data, int64_t n, int64_t per = 1) { return {data, (uint64_t)n * (uint64_t)per * 4}; }
 int elem_bytes(int dtype) { return dtype == HS2_F32 ? 4 : (dtype == HS2_BF16 ? 2 : 1); }
-Span rows_of(const hs2_cache *c) {
-  return {c->data, (uint64_t)c->num_slots * c->num_kv_heads * c->head_dim * elem_bytes(c->dtype)};
-}
-Span scales_of(const hs2_cache *c) { return words(c->scale, c->num_slots, c->num_kv_heads); }
 Span span(const hs2_tokens *x) {
   return {x->data, ((uint64_t)((int64_t)x->batch * x->tokens - 1) * x->token_stride + (uint64_t)x->num_heads * x->head_dim) *
                        elem_bytes(x->dtype)};
@@ -94,9 +90,16 @@ bool overlap(const hs2_tokens *a, const hs2_tokens *b) {
   if (off < 0) off += row;
   return off < (int64_t)a->num_heads * a->head_dim * es || off + (int64_t)b->num_heads * b->head_dim * es > row;
 }
-// K and V (and their scales) of a call that writes them
-int check_written(const hs2_cache *k, const hs2_cache *v) {
-  if (overlap(rows_of(k), rows_of(v)) || overlap(scales_of(k), scales_of(v)))
+// K and V (and their scales) of a call that writes them: apart, or pages of one pool that lie whole pages from each
+// other (every other page K's and V's), which the page table keeps apart.
+int check_written(const hs2_cache *k, const hs2_cache *v, bool paged) {
+  auto mixed = [&](const void *a, const void *b, uint64_t slot_bytes) {
+    const uint64_t all = (uint64_t)k->num_slots * slot_bytes;
+    const int64_t off = (int64_t)(reinterpret_cast<intptr_t>(b) - reinterpret_cast<intptr_t>(a));
+    return overlap(Span{a, all}, Span{b, all}) && !(paged && off != 0 && off % (int64_t)(slot_bytes * k->page_size) == 0);
+  };
+  if (mixed(k->data, v->data, (uint64_t)k->num_kv_heads * k->head_dim * elem_bytes(k->dtype)) ||
+      mixed(k->scale, v->scale, (uint64_t)k->num_kv_heads * 4))
     return fail(HS2_ERR_INVALID_ARG, "the K and V caches overlap");
   return HS2_OK;
 }
@@ -174,16 +177,13 @@ int hs2_rope_append(const hs2_tokens *q, const hs2_tokens *k, const hs2_tokens *
     return fail(HS2_ERR_UNSUPPORTED, "rot_dim %d (a multiple of 16, at most head_dim %d)", rot_dim, k_cache->head_dim);
   int64_t t_cap;
   if ((rc = check_pages(k_cache, page_table, max_pages, k->batch, &t_cap))) return rc;
-  if ((rc = check_written(k_cache, v_cache))) return rc;
-  const Span caches[4] = {rows_of(k_cache), rows_of(v_cache), scales_of(k_cache), scales_of(v_cache)};
-  for (const Span &c : caches)
-    if (overlap(c, {span(k), span(v)}) || (q && overlap(c, span(q)))) return fail(HS2_ERR_INVALID_ARG, "q, k or v overlaps a cache");
+  if ((rc = check_written(k_cache, v_cache, page_table != nullptr))) return rc;
   if (q) {
     hs2_tokens o = *q;
     o.data = q_out;
     o.token_stride = (int64_t)q->num_heads * q->head_dim;
-    if (overlap(span(&o), {caches[0], caches[1], caches[2], caches[3], span(k), span(v)}) || (!same(q_out, q->data) && overlap(&o, q)))
-      return fail(HS2_ERR_INVALID_ARG, "q_out overlaps q in part, or k, v or a cache");
+    if (overlap(&o, k) || overlap(&o, v) || (!same(q_out, q->data) && overlap(&o, q)))
+      return fail(HS2_ERR_INVALID_ARG, "q_out overlaps k, v or a part of q");
   }
   RopeParams p{};
   p.q = q ? q->data : nullptr;
@@ -333,7 +333,7 @@ int hs2_tree_accept(const hs2_cache *k_cache, const hs2_cache *v_cache, const in
   if (overlap(words(lens_out, batch), {words(seq_lens, batch), words(num_draft, batch), words(path_len, batch),
                                        words(path, batch, max_path), words(page_table, batch, max_pages)}))
     return fail(HS2_ERR_INVALID_ARG, "lens_out overlaps seq_lens, num_draft, path, path_len or page_table");
-  if ((rc = check_written(k_cache, v_cache))) return rc;
+  if ((rc = check_written(k_cache, v_cache, page_table != nullptr))) return rc;
   p.k = const_cast<void *>(k_cache->data);
   p.v = const_cast<void *>(v_cache->data);
   p.k_scale = const_cast<float *>(k_cache->scale);
@@ -374,7 +374,7 @@ int hs2_cache_evict(const hs2_cache *k_cache, const hs2_cache *v_cache, const in
   if (overlap(words(kept, units, budget), {words(seq_lens, batch), words(page_table, batch, max_pages), words(lens_out, batch),
                                            words(acc, units, acc_stride)}))
     return fail(HS2_ERR_INVALID_ARG, "kept overlaps seq_lens, page_table, lens_out or acc");
-  if ((rc = check_written(k_cache, v_cache))) return rc;
+  if ((rc = check_written(k_cache, v_cache, page_table != nullptr))) return rc;
   p.k = const_cast<void *>(k_cache->data);
   p.v = const_cast<void *>(v_cache->data);
   p.k_scale = const_cast<float *>(k_cache->scale);

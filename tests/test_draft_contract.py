@@ -60,15 +60,22 @@ def test_calls_that_write_refuse_k_and_v_in_the_same_memory(libhs2):
     """K and V rows written side by side in one memory would overwrite each other."""
     e4m3 = dict(dtype=2)
     for kc, vc in ((cache(data=A[0]), cache(data=A[0])), (cache(data=A[0]), cache(data=A[0] + (1 << 25) - 256)),
-                   (cache(data=A[0], scale=A[2], **e4m3), cache(data=A[1], scale=A[2] + 4, **e4m3))):
+                   (cache(data=A[0], scale=A[2], **e4m3), cache(data=A[1], scale=A[2] + 4, **e4m3)),
+                   (cache(data=A[0]), cache(data=A[0] + 32 * 512))):  # half a page further
         refused(abi.rope(q=None, out=None, k=abi.tokens(h=2, data=A[3]), v=abi.tokens(h=2, data=A[4]), kc=kc, vc=vc), "caches overlap")
         refused(abi.accept(kc=kc, vc=vc, lens=A[5], path=A[6], plen=A[7], out=A[8], pt=A[9]), "caches overlap")
         refused(abi.evict(kc=kc, vc=vc, lens=A[5], acc=A[6], kept=A[7], out=A[8], pt=A[9]), "caches overlap")
 
 
+def test_calls_that_write_refuse_contiguous_caches_a_sequence_apart(libhs2):
+    """Without a page table every sequence has its place in both: V's first would be K's second."""
+    kw = dict(kc=cache(data=A[0], page=1 << 14), vc=cache(data=A[0] + (512 << 14), page=1 << 14), pt=None)
+    refused(abi.accept(lens=A[5], path=A[6], plen=A[7], out=A[8], pages=1, **kw), "caches overlap")
+    refused(abi.evict(lens=A[5], acc=A[6], kept=A[7], out=A[8], pages=1, stride=1 << 14, **kw), "caches overlap")
+
+
 @pytest.mark.parametrize("kw,word", [
-    (dict(k=A[0] + 512), "overlaps a cache"), (dict(v=A[1]), "overlaps a cache"), (dict(q=A[1] + (1 << 24)), "overlaps a cache"),
-    (dict(out=A[0]), "q_out overlaps"), (dict(out=A[3] + 256), "q_out overlaps"), (dict(out=A[4]), "q_out overlaps"),
+    (dict(out=A[3] + 256), "q_out overlaps"), (dict(out=A[4]), "q_out overlaps"),
     (dict(out=A[2] + 4096), "q_out overlaps"),  # the next token's queries
     (dict(out=A[2] - 16), "q_out overlaps"),
 ])

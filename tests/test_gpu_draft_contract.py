@@ -166,6 +166,44 @@ def test_rope_append_queries_in_place_beside_keys_and_values():
     assert torch.equal(got, want) and torch.equal(same[:, :, 8:], qkv[:, :, 8:]) and torch.equal(c.k[c.slots(0, 39)], rows)
 
 
+def all_calls(c, N, lens, G, d, hkv, acc, dtype, seed):
+    """Every call of a verification step on cache c; returns what they gave."""
+    B = len(lens)
+    qkv = torch.randn(B, N, hkv * (G + 2), d, device="cuda", generator=gen(seed)).to(R.q_dtype(dtype))
+    pos = torch.arange(N, device="cuda", dtype=torch.int32).repeat(B, 1) + c.lens[:, None] - N
+    q = hs2.rope_append(qkv[:, :, :hkv * G], qkv[:, :, hkv * G:hkv * (G + 1)], qkv[:, :, hkv * (G + 1):], pos, hs2.rope_table(64),
+                        c.k, c.v, c.lens, **c.kw())
+    out = hs2.tree_attn(q, c.k, c.v, c.lens, **c.kw())
+    path = torch.tensor([[1, N - 1]] * B, dtype=torch.int32, device="cuda")
+    two = torch.full((B,), 2, dtype=torch.int32, device="cuda")
+    lens = hs2.tree_accept(c.k, c.v, c.lens, path, two, num_draft=two * 0 + N, **c.kw())
+    o, _ = hs2.full_attn_accumulate(q[:, 1].contiguous(), c.k, c.v, lens, acc, fresh=two, **c.kw())
+    lens2, kept = hs2.cache_evict(c.k, c.v, lens, acc, 100, **c.kw())
+    return [q, out, lens, o, lens2, kept, acc]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3", "f32"])
+def test_calls_on_one_pool_of_alternating_k_and_v_pages(dtype):
+    """Caches [pages, 2, page, heads, d]: K's pages the even ones, V's the odd ones of the same memory."""
+    hkv, G, d, N, page, lens = 2, 2, 128, 4, 16, [300, 70, 129]
+    apart = R.PagedCache(dtype, lens, hkv, d, page, seed=44, poison=False)
+    pool = R.PagedCache(dtype, lens, hkv, d, page, seed=44, poison=False)
+    for k, v in (("k", "v"), ("k_scale", "v_scale")):
+        if getattr(pool, k) is not None:
+            both = torch.stack([getattr(pool, x).unflatten(0, (-1, page)) for x in (k, v)], 1).flatten(0, 2)
+            setattr(pool, k, both[:-page])
+            setattr(pool, v, both[page:])
+    pool.table = apart.table * 2
+    acc = torch.rand(len(lens), hkv, apart.cap, device="cuda", generator=gen(45))
+    got = all_calls(pool, N, lens, G, d, hkv, acc.clone(), dtype, 46)
+    want = all_calls(apart, N, lens, G, d, hkv, acc.clone(), dtype, 46)
+    for x, y in zip(got, want):
+        assert torch.equal(R.bits(x), R.bits(y))
+    for name in ("k", "v", "k_scale", "v_scale"):
+        x, y = getattr(pool, name), getattr(apart, name)
+        assert x is None or torch.equal(R.bits(x.unflatten(0, (-1, page))[::2]), R.bits(y.unflatten(0, (-1, page))))
+
+
 # ---------------------------------------------------------------- rows that see nothing, drafts that nobody may see
 @pytest.mark.parametrize("dtype,N,G,d,T", [
     ("f32", 4, 2, 128, 200), ("f32", 8, 1, 64, 3000),    # one block of 8 rows
@@ -436,22 +474,6 @@ def test_rope_append_e4m3_codes_are_the_quotients():
 
 
 # ---------------------------------------------------------------- sizes at both ends
-def all_calls(c, N, lens, G, d, hkv, acc, dtype, seed):
-    """Every call of a verification step on cache c; returns what they gave."""
-    B = len(lens)
-    qkv = torch.randn(B, N, hkv * (G + 2), d, device="cuda", generator=gen(seed)).to(R.q_dtype(dtype))
-    pos = torch.arange(N, device="cuda", dtype=torch.int32).repeat(B, 1) + c.lens[:, None] - N
-    q = hs2.rope_append(qkv[:, :, :hkv * G], qkv[:, :, hkv * G:hkv * (G + 1)], qkv[:, :, hkv * (G + 1):], pos, hs2.rope_table(64),
-                        c.k, c.v, c.lens, **c.kw())
-    out = hs2.tree_attn(q, c.k, c.v, c.lens, **c.kw())
-    path = torch.tensor([[1, N - 1]] * B, dtype=torch.int32, device="cuda")
-    two = torch.full((B,), 2, dtype=torch.int32, device="cuda")
-    lens = hs2.tree_accept(c.k, c.v, c.lens, path, two, num_draft=two * 0 + N, **c.kw())
-    o, _ = hs2.full_attn_accumulate(q[:, 1].contiguous(), c.k, c.v, lens, acc, fresh=two, **c.kw())
-    lens2, kept = hs2.cache_evict(c.k, c.v, lens, acc, 100, **c.kw())
-    return [q, out, lens, o, lens2, kept, acc]
-
-
 @pytest.mark.parametrize("dtype,elements", [("bf16", 2 ** 32), ("e4m3", 2 ** 32), ("f32", 2 ** 31)])
 def test_calls_at_the_end_of_a_large_cache(dtype, elements):
     """Rows whose elements lie beyond 32 bits: the same results as in a small cache."""
