@@ -25,7 +25,7 @@ SOURCES = ["hs2_api.cu", "hs2_full_attn.cu", "hs2_select.cu", "hs2_blocks.cu", "
            "hs2_bridge.cu", "hs2_draft_api.cu", "hs2_rope.cu", "hs2_tree.cu", "hs2_tree_tc.cu",
            "hs2_accumulate.cu", "hs2_evict.cu"]
 HEADERS = ["hs2_common.cuh", "hs2_internal.h", "hs2_warp_attn.cuh", "hs2_select_common.cuh", "hs2_fused_tail.cuh",
-           "hs2_tc.cuh", "hs2_host.h", "hs2_tree_common.cuh", "hs2_rows.cuh"]
+           "hs2_tc.cuh", "hs2_host.h", "hs2_tree_common.cuh", "hs2_rows.cuh", "hs2_pair.cuh"]
 
 
 def _stale(target: str, deps) -> bool:

@@ -20,6 +20,7 @@
 // few threads, 64 us.)
 #include "hs2.h"
 #include "hs2_internal.h"
+#include "hs2_pair.cuh"
 
 namespace hs2 {
 

@@ -67,6 +67,7 @@
 
 #include "hs2.h"
 #include "hs2_internal.h"
+#include "hs2_pair.cuh"
 #include "hs2_tc.cuh"
 #include "hs2_tree_common.cuh"
 

@@ -33,3 +33,10 @@ def test_bridge_bytes():
     # hidden 4096, 4 KV heads x 128: two 4096 x 512 bf16 matrices, 4 hidden rows, 8 stored rows
     assert bench.bridge_bytes(4, 4096, 4, 128, 2, False) == 2 * 4096 * 512 * 2 + 4 * 4096 * 2 + 2 * 4 * 512 * 2
     assert bench.bridge_bytes(1, 4096, 4, 128, 1, True) == 2 * 4096 * 512 * 2 + 4096 * 2 + 2 * 512 + 2 * 4 * 4
+
+
+def test_traffic_capture_belongs_to_the_attention_sources():
+    """The committed DRAM capture is reported only for the sources that it was taken of."""
+    import bench
+
+    assert bench.measured_traffic("ctx256k_b4_bf16_paged") is not None
